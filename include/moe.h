@@ -359,6 +359,71 @@ moe_status moe_forward_partial(moe_layer_t layer, const void* x, float* partial,
  * bytes per rank).  The same bits on every rank and every run. */
 moe_status moe_combine_partials(const float* partials, void* out, int T, int H, int world, void* stream);
 
+/* ---- Operators around the layer ------------------------------------------
+ * What a model puts before, after and beside the routed experts: MXFP4 rows
+ * and grouped products over them, the block's norms, the router's balance
+ * loss.  They are stateless: every pointer is device memory of the current GPU
+ * owned by the caller, nothing is allocated or kept, calls do not wait for the
+ * GPU and can be captured in a CUDA graph, and calls on different streams or
+ * threads are independent (a `workspace` belongs to the calls of one stream at
+ * a time).  Their kernels are launched as programmatic dependents of the
+ * stream's previous work and wait for it before they touch memory.  Outputs
+ * must not overlap inputs.  Results are the same bits on every run. */
+
+/* Element types (GGML type ids). */
+typedef enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 30 } moe_type;
+
+/* MXFP4 rows (OCP microscaling: runs of 32 values, FP4 E2M1 codes under one
+ * E8M0 power of two).  For a run with largest magnitude a the scale is
+ * 2^(floor(log2 a) - 2), at least 2^-127 (the byte is its exponent + 127), and
+ * each value divided by it is rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6, ties to the even code, magnitudes above 6 to 6.  A run with an
+ * infinity or NaN gets scale byte 255 (NaN).
+ * x: [rows, cols] of `type`, row r at x + r * ld elements.  With
+ * kc = ceil(cols / 256): codes [rows, 128 kc] (16-byte aligned) and scales
+ * [rows, 8 kc] (8-byte aligned), every byte written; a run's 16 code bytes hold
+ * element j in the low and 16 + j in the high nibble of byte j, as in GGUF
+ * MXFP4 blocks; the padding has zero codes.  values: bf16 [rows, cols] or NULL,
+ * what the codes stand for (always exact in bf16).
+ * rows 0..2^24, cols 1..65536.  No counterpart on the pages (they read MXFP4
+ * files; "License and attributions"). */
+moe_status moe_mx_quantize(const void* x, moe_type type, int64_t ld, int rows, int cols, uint8_t* codes,
+                           uint8_t* scales, void* values, void* stream);
+
+/* Weights of moe_mx_product: n_mats matrices [rows, cols] as codes [n_mats,
+ * rows, 128 kc] and scales [n_mats, rows, 8 kc] (the layout of
+ * moe_mx_quantize), laid out once into `image` (16-byte aligned,
+ * moe_mx_image_bytes bytes; blocks of 256 rows x 256 columns, 34816 bytes
+ * each; rows padded to 256).  paired != 0: rows 0..rows/2-1 are gate rows and
+ * the rest their up rows (rows even), for products with SwiGLU.
+ * n_mats 1..1024, rows 1..2^20, cols 1..65536; moe_mx_image_bytes is 0
+ * outside. */
+size_t moe_mx_image_bytes(int n_mats, int rows, int cols);
+moe_status moe_mx_pack(const uint8_t* codes, const uint8_t* scales, int n_mats, int rows, int cols, int paired,
+                       void* image, void* stream);
+
+/* Grouped product, the experts' projections for a batch sorted by expert: row
+ * r of group g, offsets[g] <= r < offsets[g + 1], is
+ *   y[r, f] = sum_k w_g[f, k] * x[index[r], k]        (fp32 sums)
+ *   out[r]  = y[r]                             [rows]      paired == 0
+ *           = silu(y[r, :rows/2]) * y[r, rows/2:]  [rows/2]  paired != 0
+ * rounded once to out_type (MOE_BF16 or MOE_F32), row r at out + r * ld
+ * elements.  x: n_x rows from moe_mx_quantize.  image: from moe_mx_pack with
+ * the same n_mats, rows, cols and paired.  offsets: int32 [n_mats + 1], not
+ * decreasing, taken into 0..n_rows; NULL with n_mats == 1: all rows.  Rows of
+ * no group are left as they were.  index: int32 [n_rows] into x (NULL: row r
+ * is row r of x); an entry outside 0..n_x-1 stands for a row of zeros.
+ * Errors: INVALID_ARG, UNSUPPORTED (out_type).
+ * Source: LayerStoRm README, "License and attributions" (MXFP4 paths). */
+moe_status moe_mx_product(const uint8_t* codes, const uint8_t* scales, int n_x, const void* image, int n_mats,
+                          int rows, int cols, int paired, const int32_t* offsets, const int32_t* index, int n_rows,
+                          void* out, moe_type out_type, int64_t ld, void* stream);
+
+/* Waits for the current GPU, then reports whether a product's kernel on it gave
+ * up on a bounded wait (2 s) since the last call: MOE_ERR_CUDA, and the record
+ * is cleared; its output is invalid then. */
+moe_status moe_mx_check(void);
+
 /* Test hooks for failure detection (process-wide, off by default), read by
  * the single-token kernel at each launch.  wait_limit_ns: limit of its bounded
  * waits (0 = the default 2 s); the final wait for its own copies in flight

@@ -28,6 +28,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/moe.h"
+#include "block_ops.h"
 #include "moe_internal.h"
 
 using namespace moe;
@@ -180,6 +181,10 @@ int moe::report_error(int status, const char* msg) {
   return status;
 }
 void moe::clear_error() { g_err.clear(); }
+void moe::count_launches(unsigned n) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  g_stats.launches += n;
+}
 
 struct moe_layer {
   uint32_t id = 0;

@@ -329,6 +329,72 @@ __host__ __device__ __forceinline__ uint32_t umma_idesc_bf16(int M, int N) {
          | ((uint32_t)(M >> 4) << 24);          // M / 16
 }
 
+// ---- cp.async (per-thread asynchronous copies into shared memory) ---------------
+// 16 or 4 bytes; with `valid` false nothing is read and zeros are written.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// ---- microscaled 4-bit MMA ---------------------------------------------------------
+// D[tmem] (+)= A[smem desc] * B[smem desc], E2M1 codes with one E8M0 scale per
+// 32 values of K (64 values of K per instruction), scales in tensor memory.
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sa_tmem, uint32_t sb_tmem, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// Instruction descriptor: E2M1 A and B (K-major), E8M0 scales, fp32 D, M x N.
+// The scales of `pair` 0 or 1 are the lower or upper two bytes of a scale word.
+__host__ __device__ __forceinline__ uint32_t umma_idesc_mxf4(int M, int N, int pair) {
+  return ((uint32_t)(2 * pair) << 4)            // B scale bytes
+         | (1u << 7) | (1u << 10)               // A, B format: E2M1
+         | ((uint32_t)(N >> 3) << 17)           // N / 8
+         | (1u << 23)                           // scale format: E8M0
+         | ((uint32_t)(M >> 7) << 27)           // M / 128
+         | ((uint32_t)(2 * pair) << 29);        // A scale bytes
+}
+// 512 bytes of scales (32 rows of 16 bytes) from shared memory to four tensor
+// memory columns, the same in each of the four lane quarters.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t tmem, uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);   // start address, 16-byte units
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(128 >> 4) << 32;             // stride byte offset: next 8-row group
+  d |= (uint64_t)1 << 46;                      // descriptor version (sm_100), no swizzle
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+
+// ---- thread-block clusters -------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// every thread of every CTA of the cluster; orders their shared-memory accesses
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// float at shared-window address `a` of the cluster's CTA `rank`
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }

@@ -30,6 +30,9 @@ MOE_Q4_K = 12
 MOE_Q5_K = 13
 MOE_Q6_K = 14
 MOE_MXFP4 = 39
+MOE_F32 = 0
+MOE_F16 = 1
+MOE_BF16 = 30
 MOE_CACHE_LRU = 0
 MOE_CACHE_LFU = 1
 MOE_GATE_SOFTMAX_TOPK = 0
@@ -42,7 +45,8 @@ EXPORTS = ("moe_expert_bytes", "moe_layer_create", "moe_layer_create_mixed", "mo
            "moe_forward_host", "moe_get_routing", "moe_get_logits", "moe_prefetch",
            "moe_check", "moe_get_stats", "moe_reset_stats", "moe_set_profiling", "moe_get_profile",
            "moe_reset_profile", "moe_route_noalloc", "moe_set_test_hooks", "moe_set_expert_parallel",
-           "moe_forward_partial", "moe_combine_partials", "moe_last_error")
+           "moe_forward_partial", "moe_combine_partials", "moe_mx_quantize", "moe_mx_image_bytes", "moe_mx_pack",
+           "moe_mx_product", "moe_mx_check", "moe_last_error")
 
 KERNELS = ("router", "topk", "permute", "gate_up", "down", "combine", "prep", "small", "forward", "fused",
            "few_gate_up", "few_down")
@@ -76,6 +80,7 @@ class MoEError(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 
 
 def lib() -> ctypes.CDLL:
@@ -113,6 +118,11 @@ def lib() -> ctypes.CDLL:
             "moe_set_expert_parallel": (_I, [_P, _I, _I]),
             "moe_forward_partial": (_I, [_P, _P, _P, _I, _P]),
             "moe_combine_partials": (_I, [_P, _P, _I, _I, _I, _P]),
+            "moe_mx_quantize": (_I, [_P, _I, _L, _I, _I, _P, _P, _P, _P]),
+            "moe_mx_image_bytes": (ctypes.c_size_t, [_I, _I, _I]),
+            "moe_mx_pack": (_I, [_P, _P, _I, _I, _I, _I, _P, _P]),
+            "moe_mx_product": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _L, _P]),
+            "moe_mx_check": (_I, []),
             "moe_last_error": (ctypes.c_char_p, []),
         }
         for name, (res, args) in sig.items():
@@ -244,6 +254,31 @@ def moe_forward_partial(layer: int, x: int, partial: int, T: int, stream: int | 
 
 def moe_combine_partials(partials: int, out: int, T: int, H: int, world: int, stream: int | None = None) -> None:
     _check(lib().moe_combine_partials(partials, out, T, H, world, stream or None))
+
+
+def moe_mx_quantize(x: int, type: int, ld: int, rows: int, cols: int, codes: int, scales: int,
+                    values: int | None, stream: int | None = None) -> None:
+    _check(lib().moe_mx_quantize(x, type, ld, rows, cols, codes, scales, values or None, stream or None))
+
+
+def moe_mx_image_bytes(n_mats: int, rows: int, cols: int) -> int:
+    return int(lib().moe_mx_image_bytes(n_mats, rows, cols))
+
+
+def moe_mx_pack(codes: int, scales: int, n_mats: int, rows: int, cols: int, paired: bool, image: int,
+                stream: int | None = None) -> None:
+    _check(lib().moe_mx_pack(codes, scales, n_mats, rows, cols, 1 if paired else 0, image, stream or None))
+
+
+def moe_mx_product(codes: int, scales: int, n_x: int, image: int, n_mats: int, rows: int, cols: int, paired: bool,
+                   offsets: int | None, index: int | None, n_rows: int, out: int, out_type: int, ld: int,
+                   stream: int | None = None) -> None:
+    _check(lib().moe_mx_product(codes, scales, n_x, image, n_mats, rows, cols, 1 if paired else 0, offsets or None,
+                                index or None, n_rows, out, out_type, ld, stream or None))
+
+
+def moe_mx_check() -> None:
+    _check(lib().moe_mx_check())
 
 
 def moe_set_test_hooks(wait_limit_ns: int, hold_barrier: int) -> None:
