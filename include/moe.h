@@ -424,6 +424,80 @@ moe_status moe_mx_product(const uint8_t* codes, const uint8_t* scales, int n_x, 
  * is cleared; its output is invalid then. */
 moe_status moe_mx_check(void);
 
+/* The norms around a block with its gate and residual (one pass), per row:
+ *   z    = y / sqrt(mean(y^2) + eps) * post
+ *   out  = h + scale * gate * z
+ *   next = out / sqrt(mean(out^2) + eps) * pre     (out before its rounding)
+ * h is the residual stream, y the block's output (a forward's out), next the
+ * next block's input.  pre == NULL: no next.  post == NULL: no y, no gate, no
+ * out, and next is h's norm (before the first block).  At least one is given.
+ * Sums are fp32; out and next are rounded once to `type`. */
+typedef enum {
+  MOE_GATE_NONE = 0,    /* 1 */
+  MOE_GATE_TOKEN = 1,   /* one of `type` per row, row r at gate + r * ld_gate */
+  MOE_GATE_FEATURE = 2, /* [cols] of weight_type */
+  MOE_GATE_FULL = 3     /* [rows, cols] of `type`, row r at gate + r * ld_gate */
+} moe_gate_kind;
+typedef struct {
+  const void *h, *y;              /* [rows, cols] of `type` */
+  const void *post, *gate, *pre;  /* post, pre: [cols] of weight_type */
+  void *out, *next;               /* [rows, cols] of `type` (unused by moe_block_norm_grad) */
+  float* stats;                   /* fp32 [rows, 2], 1 / rms of y and of out: written by moe_block_norm
+                                     (may be NULL), read by moe_block_norm_grad */
+  int64_t ld_h, ld_y, ld_gate, ld_out, ld_next;   /* row strides, in elements */
+  int32_t rows, cols;             /* 0..2^24, 1..16384 */
+  int32_t type, weight_type;      /* moe_type; weights of `type` or MOE_F32 */
+  int32_t gate_kind;              /* moe_gate_kind */
+  float scale, eps;
+} moe_norm_args;
+/* Gradients, each of the type and shape of what it is the gradient of; d_h
+ * includes the residual path.  d_out NULL: zeros.  d_y and d_post only with
+ * post, d_next and d_pre only with pre, d_gate only with a gate (summed over
+ * the rows for MOE_GATE_FEATURE, over the columns for MOE_GATE_TOKEN). */
+typedef struct {
+  const void *d_out, *d_next;
+  void *d_h, *d_y, *d_post, *d_gate, *d_pre;
+  int64_t ld_d_out, ld_d_next, ld_d_h, ld_d_y, ld_d_gate;
+} moe_norm_grads;
+/* Errors: INVALID_ARG (shapes, null or misaligned pointers, a workspace below
+ * moe_block_norm_workspace bytes or not 16-byte aligned), UNSUPPORTED (types).
+ * Source: LayerStoRm README, "References" (DeepSeek-V3: a norm before each MoE
+ * block, its output added to the residual stream). */
+moe_status moe_block_norm(const moe_norm_args* args, void* stream);
+size_t moe_block_norm_workspace(int rows, int cols);
+moe_status moe_block_norm_grad(const moe_norm_args* args, const moe_norm_grads* grads, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Load-balance loss of a router over packed sequences, and per-expert counts.
+ * logits fp32 [tokens, experts], row t at logits + t * ld (moe_get_logits);
+ * ids int32 [tokens, top_k], the experts picked (moe_get_routing; an id
+ * outside 0..experts-1 is not counted); offsets int32 [seqs + 1], not
+ * decreasing: sequence s is tokens offsets[s]..offsets[s + 1] - 1 (NULL with
+ * seqs == 1: all tokens); mask uint8 [tokens], 0 = a token that does not
+ * count (NULL: all count).  With n_s the tokens of sequence s that count and
+ * p_t = softmax(l_t) (MOE_GATE_SOFTMAX_TOPK) or sigmoid(l_t) / sum of
+ * sigmoid(l_t) (MOE_GATE_SIGMOID_RENORM) over all experts (zeros where every
+ * logit is -infinity):
+ *   counts[s, i] = how often they picked expert i              int32 [seqs, experts]
+ *   f[s, i] = experts * counts[s, i] / (top_k n_s)
+ *   loss = coef * mean over s with n_s > 0 of sum_i f[s, i] * mean_t p[t, i]
+ *   slope[s, i] = coef * f[s, i] / (n_s * number of those s)   fp32 [seqs, experts]
+ * The loss is 0 without a token that counts.  moe_balance_loss_grad: the gradient
+ * of the logits, fp32 [tokens, experts], times *d_loss (device; NULL: 1),
+ * with the counts as constants; rows that do not count are zeros.
+ * tokens 0..2^24, experts 1..1024, top_k 1..32.
+ * Errors: INVALID_ARG.  Source: LayerStoRm README, "References" (DeepSeek-V3:
+ * sequence-wise balance loss); glm-flash-lite project page, "How it works"
+ * (experts ranked by how often they are used). */
+size_t moe_balance_workspace(int tokens, int experts, int seqs);
+moe_status moe_balance_loss(const float* logits, int64_t ld, const int32_t* ids, int tokens, int experts, int top_k,
+                            moe_gating gating, const int32_t* offsets, int seqs, const uint8_t* mask, float coef,
+                            float* loss, int32_t* counts, float* slope, void* workspace, size_t workspace_bytes,
+                            void* stream);
+moe_status moe_balance_loss_grad(const float* d_loss, const float* slope, const float* logits, int64_t ld, int tokens,
+                                 int experts, moe_gating gating, const int32_t* offsets, int seqs, const uint8_t* mask,
+                                 float* d_logits, int64_t ld_out, void* stream);
+
 /* Test hooks for failure detection (process-wide, off by default), read by
  * the single-token kernel at each launch.  wait_limit_ns: limit of its bounded
  * waits (0 = the default 2 s); the final wait for its own copies in flight

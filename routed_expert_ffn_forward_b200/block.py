@@ -1,7 +1,8 @@
 """Operators around the routed experts, on torch tensors.
 
 What a model puts before, after and beside ``moe_forward``: MXFP4 rows and
-grouped products over them.  The arithmetic runs in libmoe.so (include/moe.h,
+grouped products over them, the block's norms with its gate and residual, the
+router's balance loss.  The arithmetic runs in libmoe.so (include/moe.h,
 "Operators around the layer"); this module checks tensors, allocates outputs
 and passes pointers.  Every call runs on the current stream of its tensors'
 device, does not wait for the GPU and can be captured in a CUDA graph.
@@ -197,3 +198,232 @@ def mx_check() -> None:
     """Wait for the current GPU and raise MoEError if a product on it gave up on
     a bounded wait."""
     moe.moe_mx_check()
+
+
+# ---------------------------------------------------------------- the block's norms
+def _gate_kind(gate: Optional[torch.Tensor], h: torch.Tensor) -> int:
+    if gate is None:
+        return moe.MOE_GATE_NONE
+    if gate.shape == h.shape:
+        return moe.MOE_GATE_FULL
+    if gate.shape == h.shape[:1] + (1,):
+        return moe.MOE_GATE_TOKEN
+    if gate.shape == h.shape[1:]:
+        return moe.MOE_GATE_FEATURE
+    raise ValueError(f"the gate must be {tuple(h.shape)}, {(h.shape[0], 1)} or {(h.shape[1],)}, not {tuple(gate.shape)}")
+
+
+def _norm_args(h, y, post, gate, scale, pre, eps):
+    """(arguments without outputs, the tensors they point into)."""
+    kind = _type(h, "h")
+    h = _matrix(h, "h")
+    weights = post if post is not None else pre
+    if weights is None:
+        raise ValueError("neither post nor pre weights")
+    if (y is None) != (post is None) or (gate is not None and y is None):
+        raise ValueError("y and post weights come together, and a gate with them")
+    if weights.dtype not in (h.dtype, torch.float32):
+        raise ValueError(f"weights must be {h.dtype} or float32, not {weights.dtype}")
+    rows, cols = h.shape
+    a = moe.moe_norm_args(h=h.data_ptr(), ld_h=_ld(h), rows=rows, cols=cols, type=kind, weight_type=TYPES[weights.dtype],
+                          scale=scale, eps=eps)
+    a.pre = _like(pre, "pre", weights.dtype, (cols,), h.device)
+    if y is not None:
+        if y.shape != h.shape or y.dtype != h.dtype or y.device != h.device:
+            raise ValueError(f"y must be {h.dtype} {tuple(h.shape)} on {h.device}, not {y.dtype} {tuple(y.shape)} on {y.device}")
+        y = _matrix(y, "y")
+        a.y, a.ld_y = y.data_ptr(), _ld(y)
+        a.post = _like(post, "post", weights.dtype, (cols,), h.device)
+        a.gate_kind = _gate_kind(gate, h)
+        if gate is not None:
+            want = weights.dtype if a.gate_kind == moe.MOE_GATE_FEATURE else h.dtype
+            if gate.dtype != want or gate.device != h.device:
+                raise ValueError(f"this gate must be {want} on {h.device}, not {gate.dtype} on {gate.device}")
+            gate = gate.contiguous() if gate.dim() == 1 else _matrix(gate, "gate")
+            a.gate, a.ld_gate = gate.data_ptr(), _ld(gate) if gate.dim() == 2 else cols
+    return a, (h, y, gate)
+
+
+def block_norm_forward(h: torch.Tensor, y: Optional[torch.Tensor], post: Optional[torch.Tensor],
+                       gate: Optional[torch.Tensor], scale: float, pre: Optional[torch.Tensor], eps: float = 1e-6):
+    """out = h + scale * gate * rmsnorm(y) * post and next = rmsnorm(out) * pre in
+    one pass (rmsnorm(v) = v / sqrt(mean(v^2) + eps)); see ``block_norm``.
+    Returns (out, next, saved): out is None without y, next without pre; saved
+    (1/rms of both norms) is for ``block_norm_backward``."""
+    a, keep = _norm_args(h, y, post, gate, scale, pre, eps)
+    h = keep[0]
+    new = lambda: torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    out, nxt = None if y is None else new(), None if pre is None else new()
+    saved = torch.empty((h.shape[0], 2), dtype=torch.float32, device=h.device)
+    a.stats, a.ld_out, a.ld_next = saved.data_ptr(), a.cols, a.cols
+    if out is not None:
+        a.out = out.data_ptr()
+    if nxt is not None:
+        a.next = nxt.data_ptr()
+    _launch(h.device, moe.moe_block_norm, a)
+    return out, nxt, saved
+
+
+def block_norm_backward(d_out: Optional[torch.Tensor], d_next: Optional[torch.Tensor], h: torch.Tensor,
+                        y: Optional[torch.Tensor], post: Optional[torch.Tensor], gate: Optional[torch.Tensor],
+                        scale: float, pre: Optional[torch.Tensor], saved: torch.Tensor, eps: float = 1e-6):
+    """Gradients (d_h, d_y, d_post, d_gate, d_pre) of ``block_norm_forward`` with
+    the same arguments, None for what was not given.  d_out or d_next None:
+    zeros."""
+    d_pre = None
+    if d_next is None and pre is not None:   # nothing comes through the second norm
+        d_pre, pre_used = torch.zeros_like(pre), None
+        if y is None:
+            return torch.zeros_like(h), None, None, None, d_pre
+    else:
+        pre_used = pre
+    a, keep = _norm_args(h, y, post, gate, scale, pre_used, eps)
+    h, y, gate = keep
+    a.stats = _like(saved, "saved", torch.float32, (a.rows, 2), h.device)
+    g = moe.moe_norm_grads()
+    held = []
+    for name, t in (("d_out", d_out), ("d_next", d_next)):
+        if t is None:
+            continue
+        if (name == "d_next" and pre is None) or (name == "d_out" and y is None):
+            raise ValueError(f"{name} without its output")
+        if t.shape != h.shape or t.dtype != h.dtype or t.device != h.device:
+            raise ValueError(f"{name} must be {h.dtype} {tuple(h.shape)} on {h.device}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+        t = _matrix(t, name)
+        held.append(t)
+        setattr(g, name, t.data_ptr())
+        setattr(g, "ld_" + name, _ld(t))
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    d_h = new(h)
+    g.d_h, g.ld_d_h = d_h.data_ptr(), a.cols
+    d_y = d_post = d_gate = None
+    if y is not None:
+        d_y, d_post = new(y), new(post)
+        g.d_y, g.ld_d_y, g.d_post = d_y.data_ptr(), a.cols, d_post.data_ptr()
+        if gate is not None:
+            d_gate = new(gate)
+            g.d_gate, g.ld_d_gate = d_gate.data_ptr(), d_gate.shape[-1]
+    if pre_used is not None:
+        d_pre = new(pre)
+        g.d_pre = d_pre.data_ptr()
+    size = moe.moe_block_norm_workspace(a.rows, a.cols)
+    work = torch.empty(size, dtype=torch.uint8, device=h.device)
+    _launch(h.device, moe.moe_block_norm_grad, a, g, work.data_ptr(), size)
+    return d_h, d_y, d_post, d_gate, d_pre
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, y, post, gate, scale, pre, eps):
+        out, nxt, saved = block_norm_forward(h, y, post, gate, scale, pre, eps)
+        ctx.save_for_backward(h, y, post, gate, pre, saved)
+        ctx.scale, ctx.eps = scale, eps
+        ctx.set_materialize_grads(False)
+        return out, nxt
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out, d_next):
+        h, y, post, gate, pre, saved = ctx.saved_tensors
+        d_h, d_y, d_post, d_gate, d_pre = block_norm_backward(d_out, d_next, h, y, post, gate, ctx.scale, pre, saved,
+                                                              ctx.eps)
+        return d_h, d_y, d_post, d_gate, None, d_pre, None
+
+
+def block_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, post: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, scale: float = 1.0, pre: Optional[torch.Tensor] = None,
+               eps: float = 1e-6):
+    """The norms around a block with its gate and residual, differentiable:
+
+        out  = h + scale * gate * rmsnorm(y) * post
+        next = rmsnorm(out) * pre
+
+    h, y: [rows, cols], float32, float16 or bfloat16, any row stride.  post, pre:
+    [cols] of that type or float32 (both the same).  gate: [rows, cols] or
+    [rows, 1] of h's type, [cols] of the weights' type, or None.  Without y, out
+    is None and next = rmsnorm(h) * pre; without pre, next is None.  Returns
+    (out, next)."""
+    return _BlockNorm.apply(h, y, post, gate, scale, pre, eps)
+
+
+# ---------------------------------------------------------------- the balance loss
+def _balance_args(logits, gating, offsets, mask):
+    if logits.dtype != torch.float32:
+        raise ValueError(f"logits must be float32, not {logits.dtype}")
+    logits = _matrix(logits, "logits")
+    dev, tokens = logits.device, logits.shape[0]
+    if gating not in (moe.MOE_GATE_SOFTMAX_TOPK, moe.MOE_GATE_SIGMOID_RENORM):
+        raise ValueError(f"gating={gating}")
+    if offsets is not None and (offsets.dim() != 1 or len(offsets) < 2):
+        raise ValueError("offsets must hold at least two tokens' places")
+    seqs = 1 if offsets is None else len(offsets) - 1
+    off = _like(offsets, "offsets", torch.int32, (seqs + 1,), dev)
+    m = _like(mask, "mask", torch.bool, (tokens,), dev)
+    return logits, seqs, off, m
+
+
+def balance_loss_forward(logits: torch.Tensor, ids: torch.Tensor, coef: float, gating: int,
+                         offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None):
+    """The balance loss of a router (see ``balance_loss``): (loss float32 [],
+    counts int32 [seqs, experts], slope float32 [seqs, experts] for
+    ``balance_loss_backward``)."""
+    logits, seqs, off, m = _balance_args(logits, gating, offsets, mask)
+    dev = logits.device
+    tokens, experts = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, top_k]")
+    top_k = ids.shape[1]
+    i = _like(ids, "ids", torch.int32, (tokens, top_k), dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    counts = torch.empty((seqs, experts), dtype=torch.int32, device=dev)
+    slope = torch.empty((seqs, experts), dtype=torch.float32, device=dev)
+    size = moe.moe_balance_workspace(tokens, experts, seqs)
+    work = torch.empty(size, dtype=torch.uint8, device=dev)
+    _launch(dev, moe.moe_balance_loss, logits.data_ptr(), _ld(logits), i, tokens, experts, top_k, gating, off, seqs, m,
+            coef, loss.data_ptr(), counts.data_ptr(), slope.data_ptr(), work.data_ptr(), size)
+    return loss, counts, slope
+
+
+def balance_loss_backward(d_loss: Optional[torch.Tensor], slope: torch.Tensor, logits: torch.Tensor, gating: int,
+                          offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of the logits, float32 [tokens, experts], times d_loss (float32 [],
+    None: 1); zeros for tokens of no sequence and masked ones."""
+    logits, seqs, off, m = _balance_args(logits, gating, offsets, mask)
+    dev = logits.device
+    tokens, experts = logits.shape
+    s = _like(slope, "slope", torch.float32, (seqs, experts), dev)
+    d = _like(d_loss, "d_loss", torch.float32, (), dev)
+    out = torch.empty((tokens, experts), dtype=torch.float32, device=dev)
+    _launch(dev, moe.moe_balance_loss_grad, d, s, logits.data_ptr(), _ld(logits), tokens, experts, gating, off, seqs, m,
+            out.data_ptr(), experts)
+    return out
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, coef, gating, offsets, mask):
+        loss, counts, slope = balance_loss_forward(logits, ids, coef, gating, offsets, mask)
+        ctx.save_for_backward(logits, slope, offsets, mask)
+        ctx.gating = gating
+        ctx.mark_non_differentiable(counts)
+        return loss, counts
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_loss, _):
+        logits, slope, offsets, mask = ctx.saved_tensors
+        return balance_loss_backward(d_loss, slope, logits, ctx.gating, offsets, mask), None, None, None, None, None
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, gating: int,
+                 offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None):
+    """Load-balance loss of the router and per-expert counts, differentiable in
+    the logits: (loss float32 [], counts int32 [seqs, experts]).
+
+    logits: float32 [tokens, experts] (``MoELayer.logits``).  ids: int32 [tokens,
+    top_k] (``MoELayer.routing``).  gating: MOE_GATE_SOFTMAX_TOPK or
+    MOE_GATE_SIGMOID_RENORM, the probabilities' form.  offsets: int32 [seqs + 1],
+    packed sequences (None: one of all tokens); the loss is the mean over those
+    with tokens.  mask: bool [tokens], False for tokens that do not count."""
+    return _BalanceLoss.apply(logits, ids, coef, gating, offsets, mask)

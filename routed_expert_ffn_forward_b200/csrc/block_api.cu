@@ -58,6 +58,61 @@ bool mx_shape(int n_mats, int rows, int cols) {
   return n_mats >= 1 && n_mats <= kMaxMats && rows >= 1 && rows <= kMaxMxRows && cols >= 1 && cols <= kMaxMxCols;
 }
 
+// Checks of a block norm's shapes, types and pointers; fills the kernels' form.
+moe_status norm_args(const moe_norm_args* p, bool grad, NormArgs* a) {
+  if (!p) return fail(MOE_ERR_INVALID_ARG, "null arguments");
+  if (p->rows < 0 || p->rows > kMaxRows || p->cols < 1 || p->cols > 16384)
+    return fail(MOE_ERR_INVALID_ARG, "rows=%d cols=%d (0..2^24, 1..16384)", p->rows, p->cols);
+  if (!known_type(p->type) || (p->weight_type != p->type && p->weight_type != MOE_F32))
+    return fail(MOE_ERR_UNSUPPORTED, "type %d with weights of type %d (F32=0, F16=1 or BF16=30; weights the same or F32)",
+                (int)p->type, (int)p->weight_type);
+  if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_FULL)
+    return fail(MOE_ERR_INVALID_ARG, "gate_kind=%d", (int)p->gate_kind);
+  // without rows there is nothing to point at: the weights tell which norms there are
+  const bool post = p->post != nullptr, pre = p->pre != nullptr, rows = p->rows > 0;
+  if (!post && !pre) return fail(MOE_ERR_INVALID_ARG, "neither post nor pre weights");
+  if (!post && (p->y || p->gate_kind != MOE_GATE_NONE)) return fail(MOE_ERR_INVALID_ARG, "y or a gate without post weights");
+  if (rows && (!p->h || (post && !p->y) || (!grad && post && !p->out) || (!grad && pre && !p->next) || (grad && !p->stats)))
+    return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (p->gate_kind != MOE_GATE_NONE && !p->gate && (rows || p->gate_kind == MOE_GATE_FEATURE))
+    return fail(MOE_ERR_INVALID_ARG, "null gate");
+  if (p->ld_h < p->cols || (post && p->ld_y < p->cols) || (p->gate_kind == MOE_GATE_FULL && p->ld_gate < p->cols) ||
+      (p->gate_kind == MOE_GATE_TOKEN && p->ld_gate < 1) || (!grad && post && p->ld_out < p->cols) ||
+      (!grad && pre && p->ld_next < p->cols))
+    return fail(MOE_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  const size_t t = type_bytes(p->type), w = type_bytes(p->weight_type);
+  if (!aligned(p->h, t) || !aligned(p->y, t) || !aligned(p->out, t) || !aligned(p->next, t) || !aligned(p->post, w) ||
+      !aligned(p->pre, w) || !aligned(p->gate, p->gate_kind == MOE_GATE_FEATURE ? w : t) || !aligned(p->stats, 4))
+    return fail(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+  a->h = p->h;
+  a->y = post ? p->y : nullptr;
+  a->post = p->post;
+  a->gate = p->gate;
+  a->pre = p->pre;
+  a->out = p->out;
+  a->next = p->next;
+  a->stats = p->stats;
+  a->ld_h = p->ld_h;
+  a->ld_y = p->ld_y;
+  a->ld_gate = p->ld_gate;
+  a->ld_out = p->ld_out;
+  a->ld_next = p->ld_next;
+  a->rows = p->rows;
+  a->cols = p->cols;
+  a->type = p->type;
+  a->weight_type = p->weight_type;
+  a->gate_kind = p->gate_kind;
+  a->has_post = post;
+  a->scale = p->scale;
+  a->eps = p->eps;
+  auto vec = [](const void* q, int64_t ld) { return aligned(q, 16) && ld % 8 == 0; };
+  a->wide = p->cols % 8 == 0 && vec(p->h, p->ld_h) && aligned(p->post, 16) && aligned(p->pre, 16) &&
+            (!post || vec(p->y, p->ld_y)) && (p->gate_kind != MOE_GATE_FULL || vec(p->gate, p->ld_gate)) &&
+            (p->gate_kind != MOE_GATE_FEATURE || aligned(p->gate, 16)) &&
+            (grad || ((!post || vec(p->out, p->ld_out)) && (!pre || vec(p->next, p->ld_next))));
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -146,6 +201,140 @@ moe_status moe_mx_check(void) {
   }
   if (flags) return fail(MOE_ERR_CUDA, "an MXFP4 product gave up waiting (flags 0x%x)", flags);
   return MOE_OK;
+}
+
+moe_status moe_block_norm(const moe_norm_args* args, void* stream) {
+  clear_error();
+  NormArgs a;
+  const moe_status s = norm_args(args, false, &a);
+  if (s != MOE_OK || a.rows == 0) return s;
+  return launched(launch_norm(a, static_cast<cudaStream_t>(stream)), 1, "block norm");
+}
+
+size_t moe_block_norm_workspace(int rows, int cols) {
+  if (rows < 0 || rows > kMaxRows || cols < 1 || cols > 16384) return 0;
+  return (size_t)norm_grad_parts(rows, cols) * 3 * ((cols + 7) / 8 * 8) * 4;
+}
+
+moe_status moe_block_norm_grad(const moe_norm_args* args, const moe_norm_grads* g, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  clear_error();
+  NormGradArgs a;
+  const moe_status s = norm_args(args, true, &a.f);
+  if (s != MOE_OK) return s;
+  if (!g) return fail(MOE_ERR_INVALID_ARG, "null gradients");
+  const NormArgs& f = a.f;
+  const bool post = f.has_post, pre = f.pre != nullptr, gate = f.gate_kind != MOE_GATE_NONE, rows = f.rows > 0;
+  if ((rows && (!g->d_h || (post && !g->d_y) || (pre && !g->d_next))) || (post && !g->d_post) || (pre && !g->d_pre) ||
+      (gate && !g->d_gate && (rows || f.gate_kind == MOE_GATE_FEATURE)) || !workspace)
+    return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if ((g->d_out && g->ld_d_out < f.cols) || g->ld_d_h < f.cols || (pre && g->ld_d_next < f.cols) ||
+      (post && g->ld_d_y < f.cols) || (f.gate_kind == MOE_GATE_FULL && g->ld_d_gate < f.cols) ||
+      (f.gate_kind == MOE_GATE_TOKEN && g->ld_d_gate < 1))
+    return fail(MOE_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  const size_t t = type_bytes(f.type), w = type_bytes(f.weight_type);
+  if (!aligned(g->d_out, t) || !aligned(g->d_next, t) || !aligned(g->d_h, t) || !aligned(g->d_y, t) ||
+      !aligned(g->d_post, w) || !aligned(g->d_pre, w) ||
+      !aligned(g->d_gate, f.gate_kind == MOE_GATE_FEATURE ? w : t) || !aligned(workspace, 16))
+    return fail(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its type, or the workspace not to 16 bytes");
+  if (workspace_bytes < moe_block_norm_workspace(f.rows, f.cols))
+    return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                moe_block_norm_workspace(f.rows, f.cols));
+  a.d_out = g->d_out;
+  a.d_next = g->d_next;
+  a.d_h = g->d_h;
+  a.d_y = g->d_y;
+  a.d_post = g->d_post;
+  a.d_gate = g->d_gate;
+  a.d_pre = g->d_pre;
+  a.ld_d_out = g->ld_d_out;
+  a.ld_d_next = g->ld_d_next;
+  a.ld_d_h = g->ld_d_h;
+  a.ld_d_y = g->ld_d_y;
+  a.ld_d_gate = g->ld_d_gate;
+  a.partial = static_cast<float*>(workspace);
+  a.n_parts = norm_grad_parts(f.rows, f.cols);
+  a.n_sums = (post ? 1 : 0) + (pre ? 1 : 0) + (f.gate_kind == MOE_GATE_FEATURE ? 1 : 0);
+  auto vec = [](const void* q, int64_t ld) { return aligned(q, 16) && ld % 8 == 0; };
+  a.f.wide = f.wide && vec(g->d_h, g->ld_d_h) && (!g->d_out || vec(g->d_out, g->ld_d_out)) &&
+             (!pre || vec(g->d_next, g->ld_d_next)) && (!post || vec(g->d_y, g->ld_d_y)) &&
+             (f.gate_kind != MOE_GATE_FULL || vec(g->d_gate, g->ld_d_gate));
+  return launched(launch_norm_grad(a, static_cast<cudaStream_t>(stream)), 2, "block norm gradient");
+}
+
+size_t moe_balance_workspace(int tokens, int experts, int seqs) {
+  if (tokens < 0 || tokens > kMaxRows || experts < 1 || experts > 1024 || seqs < 1 || seqs > kMaxRows) return 0;
+  return balance_workspace(tokens, experts, seqs);
+}
+
+moe_status moe_balance_loss(const float* logits, int64_t ld, const int32_t* ids, int tokens, int experts, int top_k,
+                            moe_gating gating, const int32_t* offsets, int seqs, const uint8_t* mask, float coef,
+                            float* loss, int32_t* counts, float* slope, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  clear_error();
+  if (tokens < 0 || tokens > kMaxRows || experts < 1 || experts > 1024 || top_k < 1 || top_k > 32 || ld < experts)
+    return fail(MOE_ERR_INVALID_ARG, "tokens=%d experts=%d top_k=%d ld=%lld", tokens, experts, top_k, (long long)ld);
+  if (gating != MOE_GATE_SOFTMAX_TOPK && gating != MOE_GATE_SIGMOID_RENORM)
+    return fail(MOE_ERR_INVALID_ARG, "gating=%d", (int)gating);
+  if (seqs < 1 || seqs > kMaxRows || (!offsets && seqs != 1))
+    return fail(MOE_ERR_INVALID_ARG, "seqs=%d%s", seqs, offsets ? "" : " without offsets");
+  if ((tokens && (!logits || !ids)) || !loss || !counts || !slope || !workspace)
+    return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(offsets, 4) || !aligned(loss, 4) || !aligned(counts, 4) ||
+      !aligned(slope, 4) || !aligned(workspace, 4))
+    return fail(MOE_ERR_INVALID_ARG, "pointers must be aligned to 4 bytes");
+  if (workspace_bytes < balance_workspace(tokens, experts, seqs))
+    return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                balance_workspace(tokens, experts, seqs));
+  BalanceArgs a = {};
+  a.logits = logits;
+  a.ids = ids;
+  a.offsets = offsets;
+  a.mask = mask;
+  a.ld = ld;
+  a.tokens = tokens;
+  a.experts = experts;
+  a.top_k = top_k;
+  a.seqs = seqs;
+  a.gating = gating;
+  a.coef = coef;
+  a.loss = loss;
+  a.counts = counts;
+  a.slope = slope;
+  a.partial = static_cast<float*>(workspace);
+  return launched(launch_balance(a, static_cast<cudaStream_t>(stream)), balance_launches(tokens, seqs, offsets != nullptr),
+                  "balance loss");
+}
+
+moe_status moe_balance_loss_grad(const float* d_loss, const float* slope, const float* logits, int64_t ld, int tokens,
+                                 int experts, moe_gating gating, const int32_t* offsets, int seqs, const uint8_t* mask,
+                                 float* d_logits, int64_t ld_out, void* stream) {
+  clear_error();
+  if (tokens < 0 || tokens > kMaxRows || experts < 1 || experts > 1024 || ld < experts || ld_out < experts)
+    return fail(MOE_ERR_INVALID_ARG, "tokens=%d experts=%d ld=%lld ld_out=%lld", tokens, experts, (long long)ld,
+                (long long)ld_out);
+  if (gating != MOE_GATE_SOFTMAX_TOPK && gating != MOE_GATE_SIGMOID_RENORM)
+    return fail(MOE_ERR_INVALID_ARG, "gating=%d", (int)gating);
+  if (seqs < 1 || seqs > kMaxRows || (!offsets && seqs != 1))
+    return fail(MOE_ERR_INVALID_ARG, "seqs=%d%s", seqs, offsets ? "" : " without offsets");
+  if (tokens == 0) return MOE_OK;
+  if (!slope || !logits || !d_logits) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(d_loss, 4) || !aligned(slope, 4) || !aligned(logits, 4) || !aligned(offsets, 4) || !aligned(d_logits, 4))
+    return fail(MOE_ERR_INVALID_ARG, "pointers must be aligned to 4 bytes");
+  BalanceGradArgs a = {};
+  a.logits = logits;
+  a.slope = slope;
+  a.d_loss = d_loss;
+  a.offsets = offsets;
+  a.mask = mask;
+  a.ld = ld;
+  a.ld_out = ld_out;
+  a.tokens = tokens;
+  a.experts = experts;
+  a.seqs = seqs;
+  a.gating = gating;
+  a.d_logits = d_logits;
+  return launched(launch_balance_grad(a, static_cast<cudaStream_t>(stream)), 1, "balance loss gradient");
 }
 
 }  // extern "C"

@@ -78,4 +78,55 @@ cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t st);
 // call (waits for the current device)
 cudaError_t mx_product_errors(unsigned* flags);
 
+// ---- block norms ---------------------------------------------------------------
+enum { kGateNone = 0, kGateToken = 1, kGateFeature = 2, kGateFull = 3 };
+struct NormArgs {
+  const void *h, *y, *post, *gate, *pre;   // y null: no block output; pre null: no norm behind it
+  void *out, *next;
+  float* stats;                            // [rows][2] 1/rms of y and of out, or null
+  int64_t ld_h, ld_y, ld_gate, ld_out, ld_next;
+  int rows, cols, type, weight_type, gate_kind;
+  float scale, eps;
+  bool has_post;                           // a norm of y (y is null without rows)
+  bool wide;                               // 16-byte accesses: cols and every ld a multiple of 8, bases aligned
+};
+struct NormGradArgs {
+  NormArgs f;                              // out and next unused
+  const void *d_out, *d_next;              // d_out null: zeros
+  void *d_h, *d_y, *d_post, *d_gate, *d_pre;
+  int64_t ld_d_out, ld_d_next, ld_d_h, ld_d_y, ld_d_gate;
+  float* partial;                          // [n_parts][n_sums][cols to 8]
+  int n_parts, n_sums;
+};
+int norm_grad_parts(int rows, int cols);
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_grad(const NormGradArgs& a, cudaStream_t st);
+
+// ---- balance loss --------------------------------------------------------------
+struct BalanceArgs {
+  const float* logits;       // [tokens, ld]
+  const int* ids;            // [tokens, top_k]
+  const int* offsets;        // [seqs + 1] or null (one sequence)
+  const uint8_t* mask;       // [tokens] or null
+  int64_t ld;
+  int tokens, experts, top_k, seqs, gating;
+  float coef;
+  float* loss;               // [1]
+  int* counts;               // [seqs, experts]
+  float* slope;              // [seqs, experts] d loss / d probability
+  float* partial;            // workspace
+};
+struct BalanceGradArgs {
+  const float *logits, *slope, *d_loss;
+  const int* offsets;
+  const uint8_t* mask;
+  int64_t ld, ld_out;
+  int tokens, experts, seqs, gating;
+  float* d_logits;
+};
+size_t balance_workspace(int tokens, int experts, int seqs);
+int balance_launches(int tokens, int seqs, bool packed);
+cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t st);
+cudaError_t launch_balance_grad(const BalanceGradArgs& a, cudaStream_t st);
+
 }  // namespace moe

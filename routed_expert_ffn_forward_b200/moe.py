@@ -33,6 +33,10 @@ MOE_MXFP4 = 39
 MOE_F32 = 0
 MOE_F16 = 1
 MOE_BF16 = 30
+MOE_GATE_NONE = 0
+MOE_GATE_TOKEN = 1
+MOE_GATE_FEATURE = 2
+MOE_GATE_FULL = 3
 MOE_CACHE_LRU = 0
 MOE_CACHE_LFU = 1
 MOE_GATE_SOFTMAX_TOPK = 0
@@ -46,7 +50,8 @@ EXPORTS = ("moe_expert_bytes", "moe_layer_create", "moe_layer_create_mixed", "mo
            "moe_check", "moe_get_stats", "moe_reset_stats", "moe_set_profiling", "moe_get_profile",
            "moe_reset_profile", "moe_route_noalloc", "moe_set_test_hooks", "moe_set_expert_parallel",
            "moe_forward_partial", "moe_combine_partials", "moe_mx_quantize", "moe_mx_image_bytes", "moe_mx_pack",
-           "moe_mx_product", "moe_mx_check", "moe_last_error")
+           "moe_mx_product", "moe_mx_check", "moe_block_norm", "moe_block_norm_workspace", "moe_block_norm_grad",
+           "moe_balance_workspace", "moe_balance_loss", "moe_balance_loss_grad", "moe_last_error")
 
 KERNELS = ("router", "topk", "permute", "gate_up", "down", "combine", "prep", "small", "forward", "fused",
            "few_gate_up", "few_down")
@@ -69,6 +74,18 @@ class moe_profile(ctypes.Structure):
         return {"forwards": int(self.forwards),
                 "ms": {k: float(self.ms[i]) for i, k in enumerate(KERNELS)},
                 "launches": {k: int(self.launches[i]) for i, k in enumerate(KERNELS)}}
+
+
+class moe_norm_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("h", "y", "post", "gate", "pre", "out", "next", "stats")]
+                + [(n, ctypes.c_int64) for n in ("ld_h", "ld_y", "ld_gate", "ld_out", "ld_next")]
+                + [(n, ctypes.c_int32) for n in ("rows", "cols", "type", "weight_type", "gate_kind")]
+                + [(n, ctypes.c_float) for n in ("scale", "eps")])
+
+
+class moe_norm_grads(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("d_out", "d_next", "d_h", "d_y", "d_post", "d_gate", "d_pre")]
+                + [(n, ctypes.c_int64) for n in ("ld_d_out", "ld_d_next", "ld_d_h", "ld_d_y", "ld_d_gate")])
 
 
 class MoEError(RuntimeError):
@@ -123,6 +140,14 @@ def lib() -> ctypes.CDLL:
             "moe_mx_pack": (_I, [_P, _P, _I, _I, _I, _I, _P, _P]),
             "moe_mx_product": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _L, _P]),
             "moe_mx_check": (_I, []),
+            "moe_block_norm": (_I, [ctypes.POINTER(moe_norm_args), _P]),
+            "moe_block_norm_workspace": (ctypes.c_size_t, [_I, _I]),
+            "moe_block_norm_grad": (_I, [ctypes.POINTER(moe_norm_args), ctypes.POINTER(moe_norm_grads), _P,
+                                         ctypes.c_size_t, _P]),
+            "moe_balance_workspace": (ctypes.c_size_t, [_I, _I, _I]),
+            "moe_balance_loss": (_I, [_P, _L, _P, _I, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _P, _P, _P,
+                                      ctypes.c_size_t, _P]),
+            "moe_balance_loss_grad": (_I, [_P, _P, _P, _L, _I, _I, _I, _P, _I, _P, _P, _L, _P]),
             "moe_last_error": (ctypes.c_char_p, []),
         }
         for name, (res, args) in sig.items():
@@ -279,6 +304,38 @@ def moe_mx_product(codes: int, scales: int, n_x: int, image: int, n_mats: int, r
 
 def moe_mx_check() -> None:
     _check(lib().moe_mx_check())
+
+
+def moe_block_norm(args: moe_norm_args, stream: int | None = None) -> None:
+    _check(lib().moe_block_norm(ctypes.byref(args), stream or None))
+
+
+def moe_block_norm_workspace(rows: int, cols: int) -> int:
+    return int(lib().moe_block_norm_workspace(rows, cols))
+
+
+def moe_block_norm_grad(args: moe_norm_args, grads: moe_norm_grads, workspace: int, workspace_bytes: int,
+                        stream: int | None = None) -> None:
+    _check(lib().moe_block_norm_grad(ctypes.byref(args), ctypes.byref(grads), workspace, workspace_bytes,
+                                     stream or None))
+
+
+def moe_balance_workspace(tokens: int, experts: int, seqs: int) -> int:
+    return int(lib().moe_balance_workspace(tokens, experts, seqs))
+
+
+def moe_balance_loss(logits: int, ld: int, ids: int, tokens: int, experts: int, top_k: int, gating: int,
+                     offsets: int | None, seqs: int, mask: int | None, coef: float, loss: int, counts: int,
+                     slope: int, workspace: int, workspace_bytes: int, stream: int | None = None) -> None:
+    _check(lib().moe_balance_loss(logits, ld, ids, tokens, experts, top_k, gating, offsets or None, seqs, mask or None,
+                                  coef, loss, counts, slope, workspace, workspace_bytes, stream or None))
+
+
+def moe_balance_loss_grad(d_loss: int | None, slope: int, logits: int, ld: int, tokens: int, experts: int,
+                          gating: int, offsets: int | None, seqs: int, mask: int | None, d_logits: int, ld_out: int,
+                          stream: int | None = None) -> None:
+    _check(lib().moe_balance_loss_grad(d_loss or None, slope, logits, ld, tokens, experts, gating, offsets or None,
+                                       seqs, mask or None, d_logits, ld_out, stream or None))
 
 
 def moe_set_test_hooks(wait_limit_ns: int, hold_barrier: int) -> None:
