@@ -22,41 +22,52 @@ TYPES = {torch.float32: moe.MOE_F32, torch.float16: moe.MOE_F16, torch.bfloat16:
 MX_CHUNK = 256   # columns per chunk of an MXFP4 row (128 code bytes, 8 scale bytes)
 
 
+# A call on a few tokens takes the GPU two or three microseconds, less than the
+# host's work around it, so that work is kept short: shapes and dtypes are read
+# once, outputs come from new_empty and empty_like (1.1 to 1.7 us, against 2.6 us
+# for torch.empty with a dtype and device), and the stream's handle is asked for
+# without building a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _launch(device: torch.device, call, *args) -> None:
     """call(*args, stream) on the device's current stream."""
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, not on {device}")
-    if device.index == torch.cuda.current_device():
-        call(*args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        call(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            call(*args, torch.cuda.current_stream().cuda_stream)
+            call(*args, _raw_stream(index))
 
 
-def _type(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in TYPES:
-        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
-    return TYPES[t.dtype]
+def _type(dtype: torch.dtype, name: str) -> int:
+    kind = TYPES.get(dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {dtype}")
+    return kind
 
 
-def _matrix(t: torch.Tensor, name: str) -> torch.Tensor:
-    """t as rows of contiguous elements (any row stride; copied if it has none)."""
+def _rows(t: torch.Tensor, name: str):
+    """(t with contiguous elements in its rows, its row stride): any row stride
+    stays as it is, other layouts are copied."""
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
-    if (t.stride(1) == 1 or t.shape[1] == 1) and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1):
-        return t
-    return t.contiguous()
+    rows, cols = t.shape
+    if t.is_contiguous():
+        return t, cols
+    ld, one = t.stride()
+    if (one == 1 or cols == 1) and (ld >= cols or rows <= 1):
+        return t, ld if rows > 1 else cols
+    return t.contiguous(), cols
 
 
-def _ld(t: torch.Tensor) -> int:
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
-
-
-def _like(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device: torch.device) -> int:
+def _like(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
     """Pointer of an optional contiguous tensor of this type, shape and device (None: 0)."""
     if t is None:
         return 0
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, "
                          f"not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -83,14 +94,14 @@ class MXWeights(NamedTuple):
 def mx_quantize(x: torch.Tensor, values: bool = False):
     """x [rows, cols] (float32, float16 or bfloat16) in MXFP4.  With ``values``
     returns (rows, what they stand for as bfloat16 [rows, cols])."""
-    kind = _type(x, "x")
-    x = _matrix(x, "x")
+    kind = _type(x.dtype, "x")
+    x, ld = _rows(x, "x")
     rows, cols = x.shape
     kc = -(-cols // MX_CHUNK)
-    codes = torch.empty((rows, 128 * kc), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, 8 * kc), dtype=torch.uint8, device=x.device)
-    v = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device) if values else None
-    _launch(x.device, moe.moe_mx_quantize, x.data_ptr(), kind, _ld(x), rows, cols, codes.data_ptr(), scales.data_ptr(),
+    codes = x.new_empty((rows, 128 * kc), dtype=torch.uint8)
+    scales = x.new_empty((rows, 8 * kc), dtype=torch.uint8)
+    v = x.new_empty((rows, cols), dtype=torch.bfloat16) if values else None
+    _launch(x.device, moe.moe_mx_quantize, x.data_ptr(), kind, ld, rows, cols, codes.data_ptr(), scales.data_ptr(),
             v.data_ptr() if values else None)
     out = MXRows(codes, scales, cols)
     return (out, v) if values else out
@@ -182,15 +193,19 @@ def mx_product(x: MXRows, weights: MXWeights, offsets: Optional[torch.Tensor] = 
         raise ValueError(f"{weights.n_mats} matrices need offsets")
     c = _like(codes, "codes", torch.uint8, (n_x, 128 * kc), dev)
     s = _like(scales, "scales", torch.uint8, (n_x, 8 * kc), dev)
-    w = _like(weights.image, "the weights' image", torch.uint8, weights.image.shape, dev)
+    w = weights.image.data_ptr()
+    if weights.image.device != dev:
+        raise ValueError(f"the weights are on {weights.image.device}, the rows on {dev}")
     off = _like(offsets, "offsets", torch.int32, (weights.n_mats + 1,), dev)
     ix = _like(index, "index", torch.int32, (n_rows,), dev)
     if out is None:
-        out = torch.empty((n_rows, feats), dtype=out_dtype, device=dev)
-    elif tuple(out.shape) != (n_rows, feats) or out.device != dev or _matrix(out, "out") is not out:
-        raise ValueError(f"out must be [{n_rows}, {feats}] with contiguous rows on {dev}")
+        out, ld = codes.new_empty((n_rows, feats), dtype=out_dtype), feats
+    else:
+        rows, ld = _rows(out, "out")
+        if out.shape != (n_rows, feats) or out.device != dev or rows is not out:
+            raise ValueError(f"out must be [{n_rows}, {feats}] with contiguous rows on {dev}")
     _launch(dev, moe.moe_mx_product, c, s, n_x, w, weights.n_mats, weights.rows, cols, weights.paired, off, ix, n_rows,
-            out.data_ptr(), TYPES[out_dtype], _ld(out))
+            out.data_ptr(), TYPES[out_dtype], ld)
     return out
 
 
@@ -201,47 +216,53 @@ def mx_check() -> None:
 
 
 # ---------------------------------------------------------------- the block's norms
-def _gate_kind(gate: Optional[torch.Tensor], h: torch.Tensor) -> int:
-    if gate is None:
-        return moe.MOE_GATE_NONE
-    if gate.shape == h.shape:
-        return moe.MOE_GATE_FULL
-    if gate.shape == h.shape[:1] + (1,):
-        return moe.MOE_GATE_TOKEN
-    if gate.shape == h.shape[1:]:
-        return moe.MOE_GATE_FEATURE
-    raise ValueError(f"the gate must be {tuple(h.shape)}, {(h.shape[0], 1)} or {(h.shape[1],)}, not {tuple(gate.shape)}")
-
-
 def _norm_args(h, y, post, gate, scale, pre, eps):
-    """(arguments without outputs, the tensors they point into)."""
-    kind = _type(h, "h")
-    h = _matrix(h, "h")
+    """(arguments without outputs, the tensors h, y and gate that they point into)."""
+    dtype, dev, shape = h.dtype, h.device, h.shape
+    kind = _type(dtype, "h")
+    h, ld = _rows(h, "h")
     weights = post if post is not None else pre
     if weights is None:
         raise ValueError("neither post nor pre weights")
     if (y is None) != (post is None) or (gate is not None and y is None):
         raise ValueError("y and post weights come together, and a gate with them")
-    if weights.dtype not in (h.dtype, torch.float32):
-        raise ValueError(f"weights must be {h.dtype} or float32, not {weights.dtype}")
-    rows, cols = h.shape
-    a = moe.moe_norm_args(h=h.data_ptr(), ld_h=_ld(h), rows=rows, cols=cols, type=kind, weight_type=TYPES[weights.dtype],
+    wtype = weights.dtype
+    if wtype != dtype and wtype != torch.float32:
+        raise ValueError(f"weights must be {dtype} or float32, not {wtype}")
+    rows, cols = shape
+    a = moe.moe_norm_args(h=h.data_ptr(), ld_h=ld, rows=rows, cols=cols, type=kind, weight_type=TYPES[wtype],
                           scale=scale, eps=eps)
-    a.pre = _like(pre, "pre", weights.dtype, (cols,), h.device)
+    if pre is not None:
+        a.pre = _like(pre, "pre", wtype, (cols,), dev)
     if y is not None:
-        if y.shape != h.shape or y.dtype != h.dtype or y.device != h.device:
-            raise ValueError(f"y must be {h.dtype} {tuple(h.shape)} on {h.device}, not {y.dtype} {tuple(y.shape)} on {y.device}")
-        y = _matrix(y, "y")
-        a.y, a.ld_y = y.data_ptr(), _ld(y)
-        a.post = _like(post, "post", weights.dtype, (cols,), h.device)
-        a.gate_kind = _gate_kind(gate, h)
+        if y.shape != shape or y.dtype != dtype or y.device != dev:
+            raise ValueError(f"y must be {dtype} {tuple(shape)} on {dev}, not {y.dtype} {tuple(y.shape)} on {y.device}")
+        y, a.ld_y = _rows(y, "y")
+        a.y = y.data_ptr()
+        a.post = _like(post, "post", wtype, (cols,), dev)
         if gate is not None:
-            want = weights.dtype if a.gate_kind == moe.MOE_GATE_FEATURE else h.dtype
-            if gate.dtype != want or gate.device != h.device:
-                raise ValueError(f"this gate must be {want} on {h.device}, not {gate.dtype} on {gate.device}")
-            gate = gate.contiguous() if gate.dim() == 1 else _matrix(gate, "gate")
-            a.gate, a.ld_gate = gate.data_ptr(), _ld(gate) if gate.dim() == 2 else cols
-    return a, (h, y, gate)
+            want = dtype
+            if gate.shape == shape:
+                a.gate_kind = moe.MOE_GATE_FULL
+            elif gate.shape == (rows, 1):
+                a.gate_kind = moe.MOE_GATE_TOKEN
+            elif gate.shape == (cols,):
+                a.gate_kind, want = moe.MOE_GATE_FEATURE, wtype
+            else:
+                raise ValueError(f"the gate must be {tuple(shape)}, {(rows, 1)} or {(cols,)}, not {tuple(gate.shape)}")
+            if gate.dtype != want or gate.device != dev:
+                raise ValueError(f"this gate must be {want} on {dev}, not {gate.dtype} on {gate.device}")
+            if want is wtype and gate.dim() == 1:
+                gate = gate.contiguous()
+            else:
+                gate, a.ld_gate = _rows(gate, "gate")
+            a.gate = gate.data_ptr()
+    return a, h, y, gate
+
+
+def _new(t: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def block_norm_forward(h: torch.Tensor, y: Optional[torch.Tensor], post: Optional[torch.Tensor],
@@ -250,18 +271,27 @@ def block_norm_forward(h: torch.Tensor, y: Optional[torch.Tensor], post: Optiona
     one pass (rmsnorm(v) = v / sqrt(mean(v^2) + eps)); see ``block_norm``.
     Returns (out, next, saved): out is None without y, next without pre; saved
     (1/rms of both norms) is for ``block_norm_backward``."""
-    a, keep = _norm_args(h, y, post, gate, scale, pre, eps)
-    h = keep[0]
-    new = lambda: torch.empty(h.shape, dtype=h.dtype, device=h.device)
-    out, nxt = None if y is None else new(), None if pre is None else new()
-    saved = torch.empty((h.shape[0], 2), dtype=torch.float32, device=h.device)
-    a.stats, a.ld_out, a.ld_next = saved.data_ptr(), a.cols, a.cols
-    if out is not None:
-        a.out = out.data_ptr()
-    if nxt is not None:
-        a.next = nxt.data_ptr()
+    a, h, y, gate = _norm_args(h, y, post, gate, scale, pre, eps)
+    out = nxt = None
+    saved = h.new_empty((a.rows, 2), dtype=torch.float32)
+    a.stats = saved.data_ptr()
+    if y is not None:
+        out = _new(h)
+        a.out, a.ld_out = out.data_ptr(), a.cols
+    if pre is not None:
+        nxt = _new(h)
+        a.next, a.ld_next = nxt.data_ptr(), a.cols
     _launch(h.device, moe.moe_block_norm, a)
     return out, nxt, saved
+
+
+def _norm_grad(t: torch.Tensor, name: str, h: torch.Tensor):
+    """(rows of an output's gradient, pointer, row stride)."""
+    if t.shape != h.shape or t.dtype != h.dtype or t.device != h.device:
+        raise ValueError(f"{name} must be {h.dtype} {tuple(h.shape)} on {h.device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    t, ld = _rows(t, name)
+    return t, t.data_ptr(), ld
 
 
 def block_norm_backward(d_out: Optional[torch.Tensor], d_next: Optional[torch.Tensor], h: torch.Tensor,
@@ -270,45 +300,33 @@ def block_norm_backward(d_out: Optional[torch.Tensor], d_next: Optional[torch.Te
     """Gradients (d_h, d_y, d_post, d_gate, d_pre) of ``block_norm_forward`` with
     the same arguments, None for what was not given.  d_out or d_next None:
     zeros."""
+    if (d_next is not None and pre is None) or (d_out is not None and y is None):
+        raise ValueError("a gradient without its output")
     d_pre = None
     if d_next is None and pre is not None:   # nothing comes through the second norm
-        d_pre, pre_used = torch.zeros_like(pre), None
+        d_pre, pre = torch.zeros_like(pre), None
         if y is None:
             return torch.zeros_like(h), None, None, None, d_pre
-    else:
-        pre_used = pre
-    a, keep = _norm_args(h, y, post, gate, scale, pre_used, eps)
-    h, y, gate = keep
-    a.stats = _like(saved, "saved", torch.float32, (a.rows, 2), h.device)
-    g = moe.moe_norm_grads()
-    held = []
-    for name, t in (("d_out", d_out), ("d_next", d_next)):
-        if t is None:
-            continue
-        if (name == "d_next" and pre is None) or (name == "d_out" and y is None):
-            raise ValueError(f"{name} without its output")
-        if t.shape != h.shape or t.dtype != h.dtype or t.device != h.device:
-            raise ValueError(f"{name} must be {h.dtype} {tuple(h.shape)} on {h.device}, "
-                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
-        t = _matrix(t, name)
-        held.append(t)
-        setattr(g, name, t.data_ptr())
-        setattr(g, "ld_" + name, _ld(t))
-    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    d_h = new(h)
-    g.d_h, g.ld_d_h = d_h.data_ptr(), a.cols
+    a, h, y, gate = _norm_args(h, y, post, gate, scale, pre, eps)
+    rows, cols = a.rows, a.cols
+    a.stats = _like(saved, "saved", torch.float32, (rows, 2), h.device)
+    d_h = _new(h)
+    g = moe.moe_norm_grads(d_h=d_h.data_ptr(), ld_d_h=cols)
     d_y = d_post = d_gate = None
-    if y is not None:
-        d_y, d_post = new(y), new(post)
-        g.d_y, g.ld_d_y, g.d_post = d_y.data_ptr(), a.cols, d_post.data_ptr()
-        if gate is not None:
-            d_gate = new(gate)
-            g.d_gate, g.ld_d_gate = d_gate.data_ptr(), d_gate.shape[-1]
-    if pre_used is not None:
-        d_pre = new(pre)
+    if d_out is not None:
+        d_out, g.d_out, g.ld_d_out = _norm_grad(d_out, "d_out", h)
+    if pre is not None:
+        d_next, g.d_next, g.ld_d_next = _norm_grad(d_next, "d_next", h)
+        d_pre = _new(pre)
         g.d_pre = d_pre.data_ptr()
-    size = moe.moe_block_norm_workspace(a.rows, a.cols)
-    work = torch.empty(size, dtype=torch.uint8, device=h.device)
+    if y is not None:
+        d_y, d_post = _new(y), _new(post)
+        g.d_y, g.ld_d_y, g.d_post = d_y.data_ptr(), cols, d_post.data_ptr()
+        if gate is not None:
+            d_gate = _new(gate)
+            g.d_gate, g.ld_d_gate = d_gate.data_ptr(), d_gate.shape[-1]
+    size = moe.moe_block_norm_workspace(rows, cols)
+    work = h.new_empty((size,), dtype=torch.uint8)
     _launch(h.device, moe.moe_block_norm_grad, a, g, work.data_ptr(), size)
     return d_h, d_y, d_post, d_gate, d_pre
 
@@ -349,18 +367,22 @@ def block_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, post: Optional
 
 # ---------------------------------------------------------------- the balance loss
 def _balance_args(logits, gating, offsets, mask):
+    """(logits' rows, their stride, tokens, experts, sequences, pointers of offsets and mask)."""
     if logits.dtype != torch.float32:
         raise ValueError(f"logits must be float32, not {logits.dtype}")
-    logits = _matrix(logits, "logits")
-    dev, tokens = logits.device, logits.shape[0]
-    if gating not in (moe.MOE_GATE_SOFTMAX_TOPK, moe.MOE_GATE_SIGMOID_RENORM):
+    logits, ld = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    if gating != moe.MOE_GATE_SOFTMAX_TOPK and gating != moe.MOE_GATE_SIGMOID_RENORM:
         raise ValueError(f"gating={gating}")
-    if offsets is not None and (offsets.dim() != 1 or len(offsets) < 2):
-        raise ValueError("offsets must hold at least two tokens' places")
-    seqs = 1 if offsets is None else len(offsets) - 1
-    off = _like(offsets, "offsets", torch.int32, (seqs + 1,), dev)
-    m = _like(mask, "mask", torch.bool, (tokens,), dev)
-    return logits, seqs, off, m
+    seqs, off, m = 1, 0, 0
+    if offsets is not None:
+        if offsets.dim() != 1 or len(offsets) < 2:
+            raise ValueError("offsets must be [seqs + 1]")
+        seqs = len(offsets) - 1
+        off = _like(offsets, "offsets", torch.int32, (seqs + 1,), logits.device)
+    if mask is not None:
+        m = _like(mask, "mask", torch.bool, (tokens,), logits.device)
+    return logits, ld, tokens, experts, seqs, off, m
 
 
 def balance_loss_forward(logits: torch.Tensor, ids: torch.Tensor, coef: float, gating: int,
@@ -368,19 +390,17 @@ def balance_loss_forward(logits: torch.Tensor, ids: torch.Tensor, coef: float, g
     """The balance loss of a router (see ``balance_loss``): (loss float32 [],
     counts int32 [seqs, experts], slope float32 [seqs, experts] for
     ``balance_loss_backward``)."""
-    logits, seqs, off, m = _balance_args(logits, gating, offsets, mask)
-    dev = logits.device
-    tokens, experts = logits.shape
+    logits, ld, tokens, experts, seqs, off, m = _balance_args(logits, gating, offsets, mask)
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, top_k]")
     top_k = ids.shape[1]
-    i = _like(ids, "ids", torch.int32, (tokens, top_k), dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    counts = torch.empty((seqs, experts), dtype=torch.int32, device=dev)
-    slope = torch.empty((seqs, experts), dtype=torch.float32, device=dev)
+    i = _like(ids, "ids", torch.int32, (tokens, top_k), logits.device)
+    loss = logits.new_empty(())
+    counts = logits.new_empty((seqs, experts), dtype=torch.int32)
+    slope = logits.new_empty((seqs, experts))
     size = moe.moe_balance_workspace(tokens, experts, seqs)
-    work = torch.empty(size, dtype=torch.uint8, device=dev)
-    _launch(dev, moe.moe_balance_loss, logits.data_ptr(), _ld(logits), i, tokens, experts, top_k, gating, off, seqs, m,
+    work = logits.new_empty((size,), dtype=torch.uint8)
+    _launch(logits.device, moe.moe_balance_loss, logits.data_ptr(), ld, i, tokens, experts, top_k, gating, off, seqs, m,
             coef, loss.data_ptr(), counts.data_ptr(), slope.data_ptr(), work.data_ptr(), size)
     return loss, counts, slope
 
@@ -389,13 +409,11 @@ def balance_loss_backward(d_loss: Optional[torch.Tensor], slope: torch.Tensor, l
                           offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of the logits, float32 [tokens, experts], times d_loss (float32 [],
     None: 1); zeros for tokens of no sequence and masked ones."""
-    logits, seqs, off, m = _balance_args(logits, gating, offsets, mask)
-    dev = logits.device
-    tokens, experts = logits.shape
-    s = _like(slope, "slope", torch.float32, (seqs, experts), dev)
-    d = _like(d_loss, "d_loss", torch.float32, (), dev)
-    out = torch.empty((tokens, experts), dtype=torch.float32, device=dev)
-    _launch(dev, moe.moe_balance_loss_grad, d, s, logits.data_ptr(), _ld(logits), tokens, experts, gating, off, seqs, m,
+    logits, ld, tokens, experts, seqs, off, m = _balance_args(logits, gating, offsets, mask)
+    s = _like(slope, "slope", torch.float32, (seqs, experts), logits.device)
+    d = _like(d_loss, "d_loss", torch.float32, (), logits.device)
+    out = _new(logits)
+    _launch(logits.device, moe.moe_balance_loss_grad, d, s, logits.data_ptr(), ld, tokens, experts, gating, off, seqs, m,
             out.data_ptr(), experts)
     return out
 
