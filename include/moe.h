@@ -373,6 +373,12 @@ moe_status moe_combine_partials(const float* partials, void* out, int T, int H, 
 /* Element types (GGML type ids). */
 typedef enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 30 } moe_type;
 
+/* Waits for the current GPU, then reports whether one of these operators'
+ * kernels on it gave up on a bounded wait (2 s, for a copy into shared memory
+ * or a tensor-core step) since the last call: MOE_ERR_CUDA, and the record is
+ * cleared; that call's output is invalid. */
+moe_status moe_block_check(void);
+
 /* MXFP4 rows (OCP microscaling: runs of 32 values, FP4 E2M1 codes under one
  * E8M0 power of two).  For a run with largest magnitude a the scale is
  * 2^(floor(log2 a) - 2), at least 2^-127 (the byte is its exponent + 127), and
@@ -418,11 +424,6 @@ moe_status moe_mx_pack(const uint8_t* codes, const uint8_t* scales, int n_mats, 
 moe_status moe_mx_product(const uint8_t* codes, const uint8_t* scales, int n_x, const void* image, int n_mats,
                           int rows, int cols, int paired, const int32_t* offsets, const int32_t* index, int n_rows,
                           void* out, moe_type out_type, int64_t ld, void* stream);
-
-/* Waits for the current GPU, then reports whether a product's kernel on it gave
- * up on a bounded wait (2 s) since the last call: MOE_ERR_CUDA, and the record
- * is cleared; its output is invalid then. */
-moe_status moe_mx_check(void);
 
 /* The norms around a block with its gate and residual (one pass), per row:
  *   z    = y / sqrt(mean(y^2) + eps) * post
@@ -485,7 +486,8 @@ moe_status moe_block_norm_grad(const moe_norm_args* args, const moe_norm_grads* 
  * The loss is 0 without a token that counts.  moe_balance_loss_grad: the gradient
  * of the logits, fp32 [tokens, experts], times *d_loss (device; NULL: 1),
  * with the counts as constants; rows that do not count are zeros.
- * tokens 0..2^24, experts 1..1024, top_k 1..32.
+ * tokens 0..2^24, experts 1..1024, top_k 1..32, seqs 1..65535; workspace
+ * aligned to 16 bytes, of moe_balance_workspace bytes.
  * Errors: INVALID_ARG.  Source: LayerStoRm README, "References" (DeepSeek-V3:
  * sequence-wise balance loss); glm-flash-lite project page, "How it works"
  * (experts ranked by how often they are used). */

@@ -209,10 +209,10 @@ def mx_product(x: MXRows, weights: MXWeights, offsets: Optional[torch.Tensor] = 
     return out
 
 
-def mx_check() -> None:
-    """Wait for the current GPU and raise MoEError if a product on it gave up on
-    a bounded wait."""
-    moe.moe_mx_check()
+def check() -> None:
+    """Wait for the current GPU and raise MoEError if one of these operators'
+    kernels on it gave up on a bounded wait since the last check."""
+    moe.moe_block_check()
 
 
 # ---------------------------------------------------------------- the block's norms

@@ -28,12 +28,16 @@ constexpr int kSmallTokens = 128;
 int run_length(int tokens) {   // tokens per CTA: at least two per warp, at most two CTAs' worth of runs per SM
   return std::max(2 * kWarps, (tokens + 2 * 148 - 1) / (2 * 148));
 }
-// Workspace: slots of 32-bit words (experts probability sums, experts counts,
-// the valid tokens), then two words per sequence (its loss, whether it has tokens).
-__host__ __device__ __forceinline__ int slot_stride(int experts) { return 2 * experts + 1; }
+// Workspace, in 32-bit words: slots of the experts' probability sums, their
+// counts and the valid tokens, each part padded to 4 words; then two words per
+// sequence and column block (its share of the loss, whether it has tokens).
+__host__ __device__ __forceinline__ int padded(int experts) { return (experts + 3) & ~3; }
+__host__ __device__ __forceinline__ int slot_stride(int experts) { return 2 * padded(experts) + 4; }
 __host__ __device__ __forceinline__ int64_t totals_at(int tokens, int experts, int seqs, int run) {
   return ((int64_t)(tokens + run - 1) / run + seqs) * slot_stride(experts);
 }
+constexpr int kBlockCols = 128;   // experts per CTA of the second step
+__host__ __device__ __forceinline__ int column_blocks(int experts) { return (experts + kBlockCols - 1) / kBlockCols; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -41,14 +45,53 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The probabilities of one token (expert lane + 32 i in p[i]); behind the last
-// expert and for a token without a finite logit zeros.  kGrad: om = d p / d l
-// over p's own share, 1 - sigmoid(l) or 1.
-template <int kPL, bool kGrad>
-__device__ __forceinline__ void probabilities(const float* __restrict__ l, int experts, int gating, float* p, float* om) {
+// Expert of this lane's value i of kPL: fours of them with kVec (16-byte
+// accesses: experts and row stride multiples of 4, rows aligned), else every 32nd.
+template <bool kVec>
+__device__ __forceinline__ int expert_of(int i) {
   const int lane = threadIdx.x & 31;
+  return kVec ? 128 * (i >> 2) + 4 * lane + (i & 3) : 32 * i + lane;
+}
+template <int kPL, bool kVec>
+__device__ __forceinline__ void load_row(const float* __restrict__ l, int experts, float other, float* v) {
+  if (kVec) {
 #pragma unroll
-  for (int i = 0; i < kPL; ++i) p[i] = lane + 32 * i < experts ? __ldg(l + lane + 32 * i) : -INFINITY;
+    for (int i = 0; i < kPL; i += 4) {
+      const int e = expert_of<true>(i);
+      float4 q = make_float4(other, other, other, other);
+      if (e < experts) q = __ldg(reinterpret_cast<const float4*>(l + e));
+      v[i] = q.x;
+      v[i + 1] = q.y;
+      v[i + 2] = q.z;
+      v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPL; ++i) v[i] = expert_of<false>(i) < experts ? __ldg(l + expert_of<false>(i)) : other;
+  }
+}
+template <int kPL, bool kVec>
+__device__ __forceinline__ void store_row(float* l, int experts, const float* v) {
+  if (kVec) {
+#pragma unroll
+    for (int i = 0; i < kPL; i += 4) {
+      const int e = expert_of<true>(i);
+      if (e < experts) *reinterpret_cast<float4*>(l + e) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPL; ++i)
+      if (expert_of<false>(i) < experts) l[expert_of<false>(i)] = v[i];
+  }
+}
+
+// A token's logits (-infinity behind the last expert) to its probabilities, in
+// place; zeros for a token without a finite logit.  kGrad: om = 1 - sigmoid(l)
+// or 1.  The exponential is the fast one (2 + 1.2 |l - max| steps of 2^-23):
+// with the exact one and IEEE division, 40 instructions a logit, the pass over
+// 65536 x 256 logits took 36 us, twice its HBM time.
+template <int kPL, bool kGrad>
+__device__ __forceinline__ void probabilities(int gating, float* p, float* om) {
   float sum = 0.f, m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kPL; ++i) m = fmaxf(m, p[i]);
@@ -59,15 +102,15 @@ __device__ __forceinline__ void probabilities(const float* __restrict__ l, int e
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
     for (int i = 0; i < kPL; ++i) {
-      p[i] = expf(p[i] - m);
+      p[i] = __expf(p[i] - m);
       sum += p[i];
       if (kGrad) om[i] = 1.f;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kPL; ++i) {
-      const float v = p[i], e = expf(-v);
-      p[i] = 1.f / (1.f + e);
+      const float v = p[i], e = __expf(-v);
+      p[i] = __fdividef(1.f, 1.f + e);   // 0 where e is out of range
       sum += p[i];
       if (kGrad) om[i] = v > 0.f ? e * p[i] : 1.f - p[i];
     }
@@ -90,30 +133,30 @@ __device__ __forceinline__ int sequence_of(const int* __restrict__ offsets, int 
   return lo;
 }
 
-// Slopes and loss of one sequence from its sums; called by a CTA.  Returns the
-// loss (times the number of live sequences) in thread 0.
-__device__ __forceinline__ float finish(const BalanceArgs& a, int s, float n, const float* s_p, const int* s_c, float* s_red) {
-  float term = 0.f;
-  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-    const float f = n > 0.f ? (float)a.experts * (float)s_c[e] / ((float)a.top_k * n) : 0.f;
-    const float slope = n > 0.f ? a.coef * f / n : 0.f;
-    a.counts[(int64_t)s * a.experts + e] = s_c[e];
-    a.slope[(int64_t)s * a.experts + e] = slope;
-    term += f > 0.f ? slope * s_p[e] : 0.f;
-  }
-  term = warp_sum(term);
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = term;
+// Slope and term of the loss of one expert of a sequence with n valid tokens.
+__device__ __forceinline__ float finish(const BalanceArgs& a, int s, int e, float n, float sum, int count) {
+  const float f = n > 0.f ? (float)a.experts * (float)count / ((float)a.top_k * n) : 0.f;
+  const float slope = n > 0.f ? a.coef * f / n : 0.f;
+  a.counts[(int64_t)s * a.experts + e] = count;
+  a.slope[(int64_t)s * a.experts + e] = slope;
+  return f > 0.f ? slope * sum : 0.f;
+}
+// Sum over the CTA, in thread 0.
+__device__ __forceinline__ float block_sum(float v, float* s_red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float v = 0.f;
+  v = 0.f;
   if (threadIdx.x == 0)
     for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += s_red[i];
   return v;
 }
 
-template <int kPL>
+template <int kPL, bool kVec>
 __global__ void __launch_bounds__(kWarps * 32) balance_runs_kernel(const BalanceArgs a, int run, int whole) {
-  extern __shared__ float s_mem[];              // [kWarps][experts] sums, [experts] counts
-  int* s_c = reinterpret_cast<int*>(s_mem + kWarps * a.experts);
+  extern __shared__ float s_mem[];              // [kWarps][padded experts] sums, [experts] counts
+  const int width = padded(a.experts);
+  int* s_c = reinterpret_cast<int*>(s_mem + kWarps * width);
   __shared__ int s_n;
   __shared__ float s_red[kWarps];
   ptx::pdl_wait();
@@ -128,96 +171,123 @@ __global__ void __launch_bounds__(kWarps * 32) balance_runs_kernel(const Balance
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) s_c[e] = 0;
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
-    float acc[kPL] = {};
+    float acc[kPL] = {}, next[kPL];
     int valid = 0;
+    // the next token's logits are on their way while this one's are summed
+    bool have = t + warp < end && (!a.mask || __ldg(a.mask + t + warp));
+    if (have) load_row<kPL, kVec>(a.logits + (t + warp) * a.ld, a.experts, -INFINITY, next);
     for (int r = t + warp; r < end; r += kWarps) {
-      if (a.mask && !__ldg(a.mask + r)) continue;
+      const bool now = have;
+      float p[kPL];
+#pragma unroll
+      for (int i = 0; i < kPL; ++i) p[i] = next[i];
+      have = r + kWarps < end && (!a.mask || __ldg(a.mask + r + kWarps));
+      if (have) load_row<kPL, kVec>(a.logits + (r + kWarps) * a.ld, a.experts, -INFINITY, next);
+      if (!now) continue;
       ++valid;
       if (lane < a.top_k) {
         const int id = __ldg(a.ids + (int64_t)r * a.top_k + lane);
         if ((unsigned)id < (unsigned)a.experts) atomicAdd(s_c + id, 1);
       }
-      float p[kPL];
-      probabilities<kPL, false>(a.logits + r * a.ld, a.experts, a.gating, p, nullptr);
+      probabilities<kPL, false>(a.gating, p, nullptr);
 #pragma unroll
       for (int i = 0; i < kPL; ++i) acc[i] += p[i];
     }
-#pragma unroll
-    for (int i = 0; i < kPL; ++i)
-      if (lane + 32 * i < a.experts) s_mem[warp * a.experts + lane + 32 * i] = acc[i];
+    store_row<kPL, kVec>(s_mem + warp * width, a.experts, acc);
     if (lane == 0 && valid) atomicAdd(&s_n, valid);
     __syncthreads();
     float* slot = a.partial + ((int64_t)blockIdx.x + s) * slot_stride(a.experts);
+    float term = 0.f;
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += s_mem[w * a.experts + e];
+      for (int w = 0; w < kWarps; ++w) v += s_mem[w * width + e];
       if (whole) {
-        s_mem[e] = v;
+        term += finish(a, 0, e, (float)s_n, v, s_c[e]);
       } else {
         slot[e] = v;
-        reinterpret_cast<int*>(slot)[a.experts + e] = s_c[e];
+        reinterpret_cast<int*>(slot)[width + e] = s_c[e];
       }
     }
     if (whole) {
-      __syncthreads();
-      const float v = finish(a, 0, (float)s_n, s_mem, s_c, s_red);
-      if (threadIdx.x == 0) *a.loss = v;
+      term = block_sum(term, s_red);
+      if (threadIdx.x == 0) *a.loss = term;
       return;
     }
-    if (threadIdx.x == 0) reinterpret_cast<int*>(slot)[2 * a.experts] = s_n;
+    if (threadIdx.x == 0) reinterpret_cast<int*>(slot)[2 * width] = s_n;
     t = end;
     __syncthreads();
   }
 }
 
-// One CTA per sequence: its slots added in order.  seqs == 1: also the loss.
-__global__ void __launch_bounds__(512) balance_sequences_kernel(const BalanceArgs a, int run) {
-  extern __shared__ float s_p[];                 // [experts] sums, [experts] counts
-  int* s_c = reinterpret_cast<int*>(s_p + a.experts);
-  __shared__ float s_red[16];
+// One CTA per 128 experts of a sequence: its slots' shares added in order, lane
+// l of a warp four experts, the warps' shares of the slots after one another.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) balance_sequences_kernel(const BalanceArgs a, int run) {
+  __shared__ float4 s_p[kSumWarps][33];
+  __shared__ int4 s_c[kSumWarps][33];
+  __shared__ int s_n;
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const int s = blockIdx.x, stride = slot_stride(a.experts);
-  int lo = a.offsets ? min(max(__ldg(a.offsets + s), 0), a.tokens) : 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = blockIdx.y, stride = slot_stride(a.experts), width = padded(a.experts);
+  const int lo = a.offsets ? min(max(__ldg(a.offsets + s), 0), a.tokens) : 0;
   const int hi = a.offsets ? min(__ldg(a.offsets + s + 1), a.tokens) : a.tokens;
-  int n = 0;
   const int c0 = lo / run, c1 = hi > lo ? (hi - 1) / run + 1 : c0;
-  for (int c = c0; c < c1; ++c) n += __ldcg(reinterpret_cast<const int*>(a.partial) + ((int64_t)c + s) * stride + 2 * a.experts);
-  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-    float v = 0.f;
-    int k = 0;
-    for (int c = c0; c < c1; ++c) {
-      const float* slot = a.partial + ((int64_t)c + s) * stride;
-      v += __ldcg(slot + e);
-      k += __ldcg(reinterpret_cast<const int*>(slot) + a.experts + e);
-    }
-    s_p[e] = v;
-    s_c[e] = k;
-  }
+  if (threadIdx.x == 0) s_n = 0;
   __syncthreads();
-  const float v = finish(a, s, (float)n, s_p, s_c, s_red);
-  if (threadIdx.x == 0) {
-    if (a.seqs == 1) {
-      *a.loss = v;
-    } else {
-      float* totals = a.partial + totals_at(a.tokens, a.experts, a.seqs, run);
-      totals[2 * s] = v;
-      totals[2 * s + 1] = n > 0 ? 1.f : 0.f;
+  const int e = blockIdx.x * kBlockCols + 4 * lane;
+  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+  int4 k = make_int4(0, 0, 0, 0);
+  int n = 0;
+#pragma unroll 4
+  for (int c = c0 + warp; c < c1; c += kSumWarps) {
+    const float* slot = a.partial + ((int64_t)c + s) * stride;
+    if (e < width) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(slot + e));
+      const int4 j = __ldcg(reinterpret_cast<const int4*>(slot + width + e));
+      p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
+      k.x += j.x; k.y += j.y; k.z += j.z; k.w += j.w;
     }
+    if (lane == 0) n += __ldcg(reinterpret_cast<const int*>(slot) + 2 * width);
+  }
+  s_p[warp][lane] = p;
+  s_c[warp][lane] = k;
+  if (lane == 0 && n) atomicAdd(&s_n, n);
+  __syncthreads();
+  if (warp >= 4) return;
+  // thread i of the first 128: expert i of the block
+  const int i = threadIdx.x, mine = blockIdx.x * kBlockCols + i;
+  float v = 0.f;
+  int cnt = 0;
+#pragma unroll 8
+  for (int w = 0; w < kSumWarps; ++w) {
+    v += reinterpret_cast<const float*>(&s_p[w][i >> 2])[i & 3];
+    cnt += reinterpret_cast<const int*>(&s_c[w][i >> 2])[i & 3];
+  }
+  float term = mine < a.experts ? finish(a, s, mine, (float)s_n, v, cnt) : 0.f;
+  term = warp_sum(term);
+  __shared__ float s_red[4];
+  if (lane == 0) s_red[warp] = term;
+  ptx::named_barrier_sync(1, 128);
+  if (i == 0) {
+    float2* totals = reinterpret_cast<float2*>(a.partial + totals_at(a.tokens, a.experts, a.seqs, run));
+    totals[(int64_t)s * gridDim.x + blockIdx.x] =
+        make_float2(s_red[0] + s_red[1] + s_red[2] + s_red[3], s_n > 0 && blockIdx.x == 0 ? 1.f : 0.f);
   }
 }
 
-// Several sequences: the mean over those with tokens.
+// The mean over the sequences with tokens; several of them: the slopes, too.
 __global__ void __launch_bounds__(512) balance_mean_kernel(const BalanceArgs a, int run) {
   __shared__ float s_v[16], s_k[16];
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const float* totals = a.partial + totals_at(a.tokens, a.experts, a.seqs, run);
+  const float2* totals = reinterpret_cast<const float2*>(a.partial + totals_at(a.tokens, a.experts, a.seqs, run));
   float v = 0.f, k = 0.f;
-  for (int s = threadIdx.x; s < a.seqs; s += blockDim.x) {
-    v += __ldcg(totals + 2 * s);
-    k += __ldcg(totals + 2 * s + 1);
+  for (int s = threadIdx.x; s < a.seqs * column_blocks(a.experts); s += blockDim.x) {
+    const float2 q = __ldcg(totals + s);
+    v += q.x;
+    k += q.y;
   }
   v = warp_sum(v);
   k = warp_sum(k);
@@ -233,60 +303,75 @@ __global__ void __launch_bounds__(512) balance_mean_kernel(const BalanceArgs a, 
   }
   const float inv = k > 0.f ? 1.f / k : 0.f;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.loss = v * inv;
+  if (a.seqs == 1) return;
   const int64_t n = (int64_t)a.seqs * a.experts;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
     a.slope[i] *= inv;
 }
 
-// One warp per run of tokens.
-template <int kPL>
+// One warp per run of tokens; the next token's logits are on their way.
+template <int kPL, bool kVec>
 __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceGradArgs a, int per_warp) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
   const int64_t first = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * per_warp;
   if (first >= a.tokens) return;
   const int t0 = (int)first, t1 = min(t0 + per_warp, a.tokens);
   const float up = a.d_loss ? __ldg(a.d_loss) : 1.f;
-  int s = sequence_of(a.offsets, a.seqs, t0);
+  int s = -1, end = t0;   // the sequence whose slopes are in k, and where it ends
+  float next[kPL], k[kPL];
+  load_row<kPL, kVec>(a.logits + t0 * a.ld, a.experts, -INFINITY, next);
   for (int t = t0; t < t1; ++t) {
-    if (a.offsets && (s < 0 || t >= __ldg(a.offsets + s + 1))) s = sequence_of(a.offsets, a.seqs, t);
-    float* out = a.d_logits + t * a.ld_out;
+    float p[kPL], om[kPL];
+#pragma unroll
+    for (int i = 0; i < kPL; ++i) p[i] = next[i];
+    if (t + 1 < t1) load_row<kPL, kVec>(a.logits + (t + 1) * a.ld, a.experts, -INFINITY, next);
+    if (t >= end) {
+      s = sequence_of(a.offsets, a.seqs, t);
+      end = !a.offsets ? a.tokens : s >= 0 ? __ldg(a.offsets + s + 1) : t + 1;
+      if (s >= 0) load_row<kPL, kVec>(a.slope + (int64_t)s * a.experts, a.experts, 0.f, k);
+    }
     if (s < 0 || (a.mask && !__ldg(a.mask + t))) {
 #pragma unroll
-      for (int i = 0; i < kPL; ++i)
-        if (lane + 32 * i < a.experts) out[lane + 32 * i] = 0.f;
-      continue;
+      for (int i = 0; i < kPL; ++i) p[i] = 0.f;
+    } else {
+      float dot = 0.f;
+      probabilities<kPL, true>(a.gating, p, om);
+#pragma unroll
+      for (int i = 0; i < kPL; ++i) dot = fmaf(k[i], p[i], dot);
+      dot = warp_sum(dot);
+#pragma unroll
+      for (int i = 0; i < kPL; ++i) p[i] *= up * (k[i] - dot) * om[i];
     }
-    float p[kPL], om[kPL], k[kPL], dot = 0.f;
-    const float* slope = a.slope + (int64_t)s * a.experts;
-#pragma unroll
-    for (int i = 0; i < kPL; ++i) k[i] = lane + 32 * i < a.experts ? up * __ldg(slope + lane + 32 * i) : 0.f;
-    probabilities<kPL, true>(a.logits + t * a.ld, a.experts, a.gating, p, om);
-#pragma unroll
-    for (int i = 0; i < kPL; ++i) dot = fmaf(k[i], p[i], dot);
-    dot = warp_sum(dot);
-#pragma unroll
-    for (int i = 0; i < kPL; ++i)
-      if (lane + 32 * i < a.experts) out[lane + 32 * i] = p[i] * (k[i] - dot) * om[i];
+    store_row<kPL, kVec>(a.d_logits + t * a.ld_out, a.experts, p);
   }
 }
 
-template <int kPL>
-cudaError_t forward(const BalanceArgs& a, cudaStream_t st) {
+bool vectors_of_4(const void* p, int64_t ld, int experts) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 4 == 0 && experts % 4 == 0;
+}
+
+template <int kPL, bool kVec>
+cudaError_t forward_as(const BalanceArgs& a, cudaStream_t st) {
   const bool whole = a.tokens <= kSmallTokens && a.seqs == 1 && !a.offsets;
   const int run = whole ? std::max(a.tokens, 1) : run_length(a.tokens), runs = std::max(1, (a.tokens + run - 1) / run);
-  const size_t smem = (size_t)(kWarps + 1) * a.experts * 4;
-  auto* kernel = balance_runs_kernel<kPL>;
+  const size_t smem = ((size_t)kWarps * padded(a.experts) + a.experts) * 4;
+  auto* kernel = balance_runs_kernel<kPL, kVec>;
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess)
     e = launch_dependent(kernel, dim3((unsigned)runs), dim3(kWarps * 32), smem, st, 1, a, run, whole ? 1 : 0);
   if (e != cudaSuccess || whole) return e;
-  e = launch_dependent(balance_sequences_kernel, dim3((unsigned)a.seqs), dim3(512), (size_t)a.experts * 8, st, 1, a, run);
-  if (e != cudaSuccess || a.seqs == 1) return e;
-  const unsigned blocks = (unsigned)std::min<int64_t>(sm_count(), ((int64_t)a.seqs * a.experts + 511) / 512);
+  e = launch_dependent(balance_sequences_kernel, dim3((unsigned)column_blocks(a.experts), (unsigned)a.seqs),
+                       dim3(kSumWarps * 32), 0, st, 1, a, run);
+  if (e != cudaSuccess) return e;
+  const unsigned blocks =
+      a.seqs == 1 ? 1 : (unsigned)std::min<int64_t>(sm_count(), ((int64_t)a.seqs * a.experts + 511) / 512);
   return launch_dependent(balance_mean_kernel, dim3(blocks), dim3(512), 0, st, 1, a, run);
+}
+template <int kPL>
+cudaError_t forward(const BalanceArgs& a, cudaStream_t st) {
+  return vectors_of_4(a.logits, a.ld, a.experts) ? forward_as<kPL, true>(a, st) : forward_as<kPL, false>(a, st);
 }
 
 template <int kPL>
@@ -294,16 +379,20 @@ cudaError_t backward(const BalanceGradArgs& a, cudaStream_t st) {
   const int warps = sm_count() * 64;
   const int per_warp = std::max(1, (a.tokens + warps - 1) / warps);
   const int blocks = ((a.tokens + per_warp - 1) / per_warp + 7) / 8;
-  return launch_dependent(balance_grad_kernel<kPL>, dim3((unsigned)blocks), dim3(256), 0, st, 1, a, per_warp);
+  if (vectors_of_4(a.logits, a.ld, a.experts) && vectors_of_4(a.d_logits, a.ld_out, a.experts) &&
+      vectors_of_4(a.slope, 0, a.experts))
+    return launch_dependent(balance_grad_kernel<kPL, true>, dim3((unsigned)blocks), dim3(256), 0, st, 1, a, per_warp);
+  return launch_dependent(balance_grad_kernel<kPL, false>, dim3((unsigned)blocks), dim3(256), 0, st, 1, a, per_warp);
 }
 
 }  // namespace
 
 size_t balance_workspace(int tokens, int experts, int seqs) {
-  return (size_t)(totals_at(tokens, experts, seqs, run_length(tokens)) + 2 * (int64_t)seqs) * 4;
+  return (size_t)(totals_at(tokens, experts, seqs, run_length(tokens)) +
+                  2 * (int64_t)seqs * column_blocks(experts)) * 4;
 }
 int balance_launches(int tokens, int seqs, bool packed) {
-  return tokens <= kSmallTokens && seqs == 1 && !packed ? 1 : seqs == 1 ? 2 : 3;
+  return tokens <= kSmallTokens && seqs == 1 && !packed ? 1 : 3;
 }
 cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t st) {
   return a.experts <= 128 ? forward<4>(a, st) : a.experts <= 256 ? forward<8>(a, st) : a.experts <= 512 ? forward<16>(a, st)

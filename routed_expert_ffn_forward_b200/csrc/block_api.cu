@@ -123,6 +123,8 @@ moe_status moe_mx_quantize(const void* x, moe_type type, int64_t ld, int rows, i
   if (rows < 0 || rows > kMaxRows || cols < 1 || cols > kMaxMxCols || ld < cols)
     return fail(MOE_ERR_INVALID_ARG, "rows=%d cols=%d ld=%lld", rows, cols, (long long)ld);
   if (!known_type(type)) return fail(MOE_ERR_UNSUPPORTED, "type %d (supported: F32=0, F16=1, BF16=30)", (int)type);
+  if ((long long)rows * mx_chunks(cols) > 0x7FFFFFFFll)
+    return fail(MOE_ERR_UNSUPPORTED, "rows=%d cols=%d: more than 2^31 chunks of 256", rows, cols);
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "null pointer");
   if (!aligned(x, type_bytes(type)) || !aligned(codes, 16) || !aligned(scales, 8) || !aligned(values, 2))
@@ -191,15 +193,18 @@ moe_status moe_mx_product(const uint8_t* codes, const uint8_t* scales, int n_x, 
   return launched(launch_mx_product(a, static_cast<cudaStream_t>(stream)), 1, "MXFP4 product");
 }
 
-moe_status moe_mx_check(void) {
+moe_status moe_block_check(void) {
   clear_error();
-  unsigned flags = 0;
-  const cudaError_t e = mx_product_errors(&flags);
+  unsigned mx = 0, norm = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = mx_product_errors(&mx);
+  if (e == cudaSuccess) e = norm_errors(&norm);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return fail(MOE_ERR_CUDA, "%s", cudaGetErrorString(e));
   }
-  if (flags) return fail(MOE_ERR_CUDA, "an MXFP4 product gave up waiting (flags 0x%x)", flags);
+  if (mx) return fail(MOE_ERR_CUDA, "an MXFP4 product gave up waiting (flags 0x%x)", mx);
+  if (norm) return fail(MOE_ERR_CUDA, "a block norm gave up waiting (flags 0x%x)", norm);
   return MOE_OK;
 }
 
@@ -253,7 +258,7 @@ moe_status moe_block_norm_grad(const moe_norm_args* args, const moe_norm_grads* 
   a.ld_d_y = g->ld_d_y;
   a.ld_d_gate = g->ld_d_gate;
   a.partial = static_cast<float*>(workspace);
-  a.n_parts = norm_grad_parts(f.rows, f.cols);
+  a.n_parts = 0;   // the launcher's choice, at most what the workspace holds
   a.n_sums = (post ? 1 : 0) + (pre ? 1 : 0) + (f.gate_kind == MOE_GATE_FEATURE ? 1 : 0);
   auto vec = [](const void* q, int64_t ld) { return aligned(q, 16) && ld % 8 == 0; };
   a.f.wide = f.wide && vec(g->d_h, g->ld_d_h) && (!g->d_out || vec(g->d_out, g->ld_d_out)) &&
@@ -263,7 +268,7 @@ moe_status moe_block_norm_grad(const moe_norm_args* args, const moe_norm_grads* 
 }
 
 size_t moe_balance_workspace(int tokens, int experts, int seqs) {
-  if (tokens < 0 || tokens > kMaxRows || experts < 1 || experts > 1024 || seqs < 1 || seqs > kMaxRows) return 0;
+  if (tokens < 0 || tokens > kMaxRows || experts < 1 || experts > 1024 || seqs < 1 || seqs > 65535) return 0;
   return balance_workspace(tokens, experts, seqs);
 }
 
@@ -276,13 +281,13 @@ moe_status moe_balance_loss(const float* logits, int64_t ld, const int32_t* ids,
     return fail(MOE_ERR_INVALID_ARG, "tokens=%d experts=%d top_k=%d ld=%lld", tokens, experts, top_k, (long long)ld);
   if (gating != MOE_GATE_SOFTMAX_TOPK && gating != MOE_GATE_SIGMOID_RENORM)
     return fail(MOE_ERR_INVALID_ARG, "gating=%d", (int)gating);
-  if (seqs < 1 || seqs > kMaxRows || (!offsets && seqs != 1))
+  if (seqs < 1 || seqs > 65535 || (!offsets && seqs != 1))
     return fail(MOE_ERR_INVALID_ARG, "seqs=%d%s", seqs, offsets ? "" : " without offsets");
   if ((tokens && (!logits || !ids)) || !loss || !counts || !slope || !workspace)
     return fail(MOE_ERR_INVALID_ARG, "null pointer");
   if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(offsets, 4) || !aligned(loss, 4) || !aligned(counts, 4) ||
-      !aligned(slope, 4) || !aligned(workspace, 4))
-    return fail(MOE_ERR_INVALID_ARG, "pointers must be aligned to 4 bytes");
+      !aligned(slope, 4) || !aligned(workspace, 16))
+    return fail(MOE_ERR_INVALID_ARG, "pointers must be aligned to 4 bytes, the workspace to 16");
   if (workspace_bytes < balance_workspace(tokens, experts, seqs))
     return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes,
                 balance_workspace(tokens, experts, seqs));
@@ -315,7 +320,7 @@ moe_status moe_balance_loss_grad(const float* d_loss, const float* slope, const 
                 (long long)ld_out);
   if (gating != MOE_GATE_SOFTMAX_TOPK && gating != MOE_GATE_SIGMOID_RENORM)
     return fail(MOE_ERR_INVALID_ARG, "gating=%d", (int)gating);
-  if (seqs < 1 || seqs > kMaxRows || (!offsets && seqs != 1))
+  if (seqs < 1 || seqs > 65535 || (!offsets && seqs != 1))
     return fail(MOE_ERR_INVALID_ARG, "seqs=%d%s", seqs, offsets ? "" : " without offsets");
   if (tokens == 0) return MOE_OK;
   if (!slope || !logits || !d_logits) return fail(MOE_ERR_INVALID_ARG, "null pointer");

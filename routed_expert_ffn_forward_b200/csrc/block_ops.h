@@ -75,7 +75,7 @@ struct MxProductArgs {
 };
 cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t st);
 // bit flags of products whose kernel gave up on a bounded wait since the last
-// call (waits for the current device)
+// call (the GPU is idle)
 cudaError_t mx_product_errors(unsigned* flags);
 
 // ---- block norms ---------------------------------------------------------------
@@ -99,6 +99,8 @@ struct NormGradArgs {
   int n_parts, n_sums;
 };
 int norm_grad_parts(int rows, int cols);
+// bit flags of kernels that gave up on a bounded wait since the last call (the GPU is idle)
+cudaError_t norm_errors(unsigned* flags);
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_grad(const NormGradArgs& a, cudaStream_t st);
 

@@ -70,43 +70,43 @@ __device__ __forceinline__ Unit find_unit(int u, const int* s_off, const int* s_
   return {lo, s_off[lo] + t * per, min(per, count - t * per), local / tiles};
 }
 
-// Two accumulators of one lane: features 2 i and 2 i + 1, or gate and up of feature i.
-__device__ __forceinline__ void store_pair(const MxProductArgs& a, int row, int i, float v0, float v1) {
-  if (a.paired) {
-    const float h = __fdividef(v0, 1.f + __expf(-v0)) * v1;   // silu(gate) * up, ~1e-6 relative
-    if (i >= a.features) return;
-    if (a.out_type == kF32)
-      static_cast<float*>(a.out)[row * a.ld + i] = h;
-    else
-      static_cast<__nv_bfloat16*>(a.out)[row * a.ld + i] = __float2bfloat16_rn(h);
-    return;
+// Where a thread's accumulators go: lane i of the unit's 128, two accumulators
+// each (features 2 i and 2 i + 1, or the gate and up of feature i).
+template <bool kPaired, typename Out>
+struct Store {
+  Out* base;     // feature of row 0
+  int64_t ld;
+  int n;         // features this lane stores: 0, 1 or 2
+  bool wide;
+  __device__ __forceinline__ Store(const MxProductArgs& a, int i) : ld(a.ld), wide(a.wide_store) {
+    const int f = kPaired ? i : 2 * i;
+    base = static_cast<Out*>(a.out) + f;
+    n = min(max(a.features - f, 0), kPaired ? 1 : 2);
   }
-  const int f = 2 * i;
-  if (f >= a.features) return;
-  const bool both = f + 1 < a.features;
-  if (a.out_type == kF32) {
-    float* p = static_cast<float*>(a.out) + row * a.ld + f;
-    if (a.wide_store && both) {
-      *reinterpret_cast<float2*>(p) = make_float2(v0, v1);
+  __device__ __forceinline__ void operator()(Out* p, float v0, float v1) const {
+    if (kPaired) {
+      const float h = __fdividef(v0, 1.f + __expf(-v0)) * v1;   // silu(gate) * up, ~1e-6 relative
+      if (n) put(p, h);
+    } else if (n == 2 && wide) {
+      put2(p, v0, v1);
     } else {
-      p[0] = v0;
-      if (both) p[1] = v1;
-    }
-  } else {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + row * a.ld + f;
-    if (a.wide_store && both) {
-      *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v0, v1);
-    } else {
-      p[0] = __float2bfloat16_rn(v0);
-      if (both) p[1] = __float2bfloat16_rn(v1);
+      if (n) put(p, v0);
+      if (n == 2) put(p + 1, v1);
     }
   }
-}
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ void put2(float* p, float v0, float v1) {
+    *reinterpret_cast<float2*>(p) = make_float2(v0, v1);
+  }
+  static __device__ __forceinline__ void put2(__nv_bfloat16* p, float v0, float v1) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v0, v1);
+  }
+};
 
-template <int kNT, int kNS, int kNAcc, bool kSplit>
+template <int kNT, int kNS, int kNAcc, bool kSplit, bool kPaired, typename Out>
 __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProductArgs a, int cluster) {
   using C = Config<kNT, kNS, kNAcc>;
-  constexpr int kLag = kNS - 2;                 // row copies a producer thread keeps in flight
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* w_full = reinterpret_cast<uint64_t*>(sm + (size_t)kNS * C::kStage);
@@ -119,12 +119,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
   int* s_warp = reinterpret_cast<int*>(s_tmem + 4);
   int* s_off = s_warp + 32;                     // [groups + 1] row offsets, in range
   int* s_start = s_off + kMaxGroups + 4;        // [groups + 1] first unit of each group
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < kNS; ++i) {
       ptx::mbar_init(&w_full[i], 1);
-      ptx::mbar_init(&r_full[i], kRowWarps);
+      ptx::mbar_init(&r_full[i], kRowWarps * 32);
       ptx::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kNAcc; ++i) {
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
   }
   if (tid == 0) s_start[a.groups] = n_units;
   __syncthreads();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
   const int rank = kSplit ? (int)ptx::cluster_rank() : 0;
   const int first = kSplit ? blockIdx.x / cluster : blockIdx.x, step = kSplit ? gridDim.x / cluster : gridDim.x;
   const int k0 = kSplit ? a.kc * rank / cluster : 0, k1 = kSplit ? a.kc * (rank + 1) / cluster : a.kc;
@@ -206,20 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
           ptx::cp_async_4(sdst + j * 512, src, srows[j] >= 0);
           ptx::cp_async_4(sdst + (C::kScaleTiles + j) * 512, src + 4, srows[j] >= 0);
         }
-        ptx::cp_async_commit();
-        if (it >= kLag) {   // step it - kLag has landed
-          ptx::cp_async_wait<kLag>();
-          ptx::fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&r_full[(it - kLag) % kNS]);
-        }
+        ptx::cp_async_arrive(&r_full[s]);
       }
     }
-    ptx::cp_async_wait<0>();
-    ptx::fence_proxy_async();
-    __syncwarp();
-    if (lane == 0 && ok)
-      for (int i = max(it - kLag, 0); i < it; ++i) ptx::mbar_arrive(&r_full[i % kNS]);
+    ptx::cp_async_commit();
+    ptx::cp_async_wait<0>();   // never leave with a copy into shared memory in flight
   } else if (warp == kWeightWarp) {
     // ------------------------------------------------------------ weights
     if (lane == 0) {
@@ -245,55 +236,58 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
       if (!ok) log.drain(w_full, kNS);   // never leave with a copy into shared memory in flight
     }
   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      int it = 0, n = 0;
-      bool ok = true;
-      for (int u = first; u < n_units && ok; u += step, ++n) {
-        const Unit un = find_unit<kNT>(u, s_off, s_start, a.groups);
-        const int acc = n % kNAcc, N = (un.count + 15) & ~15;
-        const uint32_t id0 = ptx::umma_idesc_mxf4(128, N, 0), id1 = ptx::umma_idesc_mxf4(128, N, 1);
-        const uint32_t d0 = tmem + acc * 2 * kNT, d1 = d0 + kNT;
-        if (!ptx::mbar_wait(&acc_empty[acc], ((n / kNAcc) & 1) ^ 1)) {
-          atomicOr(&g_mx_err, 4u);
+    // ------------------------------------------------------------ MMA (the whole warp; one lane's instructions)
+    const uint32_t on = ptx::elect_one();
+    const uint32_t ring = ptx::smem_u32(sm);
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = first; u < n_units && ok; u += step, ++n) {
+      const Unit un = find_unit<kNT>(u, s_off, s_start, a.groups);
+      const int acc = n % kNAcc, N = __shfl_sync(0xffffffffu, (un.count + 15) & ~15, 0);
+      const uint32_t id0 = ptx::umma_idesc_mxf4(128, N, 0), id1 = ptx::umma_idesc_mxf4(128, N, 1);
+      const uint32_t d0 = tmem + acc * 2 * kNT, d1 = d0 + kNT;
+      if (!ptx::mbar_wait(&acc_empty[acc], ((n / kNAcc) & 1) ^ 1)) {
+        if (on) atomicOr(&g_mx_err, 4u);
+        break;
+      }
+      ptx::tc_fence_after();
+      for (int k = k0; k < k1; ++k) {
+        if (!ptx::mbar_wait(&w_full[s], ph) || !ptx::mbar_wait(&r_full[s], ph)) {
+          if (on) atomicOr(&g_mx_err, 4u);
+          ok = false;
           break;
         }
+        ptx::fence_proxy_async();   // the rows came through the generic proxy
         ptx::tc_fence_after();
-        for (int k = k0; k < k1; ++k, ++it) {
-          const int s = it % kNS;
-          const uint32_t ph = (it / kNS) & 1;
-          if (!ptx::mbar_wait(&w_full[s], ph) || !ptx::mbar_wait(&r_full[s], ph)) {
-            atomicOr(&g_mx_err, 4u);
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t st = ptx::smem_u32(sm + (size_t)s * C::kStage);
-          const uint32_t wsc = st + 2 * kMxHalfCodes, rows = st + kMxBlockBytes;
-          const uint32_t rsc = rows + ((C::kRowCodes + 1023) & ~1023);
-          // scale columns: A half h, 128 of K c: kSA + 4 (2 h + c); B: kSB + 4 (c tiles + j)
+        const uint32_t st = ring + s * C::kStage, rows = st + kMxBlockBytes;
+        const uint64_t wd = ptx::umma_desc_sw128(st), rd = ptx::umma_desc_sw128(rows);
+        const uint64_t wsd = ptx::scales_desc(st + 2 * kMxHalfCodes);
+        const uint64_t rsd = ptx::scales_desc(rows + ((C::kRowCodes + 1023) & ~1023));
+        // scale columns: A half h, 128 of K c: kSA + 4 (2 h + c); B: kSB + 4 (c tiles + j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) ptx::tmem_copy_scales(tmem + C::kSA + 4 * i, wsc + 512 * i);
+        for (int i = 0; i < 4; ++i) ptx::tmem_copy_scales(on, tmem + C::kSA + 4 * i, wsd + 32 * i);
 #pragma unroll
-          for (int i = 0; i < 2 * C::kScaleTiles; ++i) ptx::tmem_copy_scales(tmem + C::kSB + 4 * i, rsc + 512 * i);
+        for (int i = 0; i < 2 * C::kScaleTiles; ++i) ptx::tmem_copy_scales(on, tmem + C::kSB + 4 * i, rsd + 32 * i);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {   // 64 of K each, 32 bytes of a row
-            const uint64_t bd = ptx::umma_desc_sw128(rows + 32 * q);
-            const uint32_t id = q & 1 ? id1 : id0, c = q >> 1;
-            const uint32_t sb = tmem + C::kSB + 4 * C::kScaleTiles * c;
-            const bool add = k > k0 || q > 0;
-            ptx::umma_mxf4(d0, ptx::umma_desc_sw128(st + 32 * q), bd, id, tmem + C::kSA + 4 * c, sb, add);
-            ptx::umma_mxf4(d1, ptx::umma_desc_sw128(st + kMxHalfCodes + 32 * q), bd, id, tmem + C::kSA + 8 + 4 * c, sb,
-                           add);
-          }
-          ptx::umma_commit(&empty[s]);
+        for (int q = 0; q < 4; ++q) {   // 64 of K each, 32 bytes of a row
+          const uint32_t id = q & 1 ? id1 : id0, c = q >> 1;
+          const uint32_t sb = tmem + C::kSB + 4 * C::kScaleTiles * c;
+          const bool add = k > k0 || q > 0;
+          ptx::umma_mxf4(on, d0, wd + 2 * q, rd + 2 * q, id, tmem + C::kSA + 4 * c, sb, add);
+          ptx::umma_mxf4(on, d1, wd + kMxHalfCodes / 16 + 2 * q, rd + 2 * q, id, tmem + C::kSA + 8 + 4 * c, sb, add);
         }
-        if (ok) ptx::umma_commit(&acc_full[acc]);
+        ptx::umma_commit_on(on, &empty[s]);
+        if (++s == kNS) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      // wait for every MMA this thread issued before TMEM is released
-      ptx::umma_commit(drain);
-      if (!ptx::mbar_wait(drain, 0)) atomicOr(&g_mx_err, 4u);
+      if (ok) ptx::umma_commit_on(on, &acc_full[acc]);
     }
+    // wait for every MMA this warp issued before TMEM is released
+    ptx::umma_commit_on(on, drain);
+    if (!ptx::mbar_wait(drain, 0) && on) atomicOr(&g_mx_err, 4u);
   } else if (warp >= kFirstEpi) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, sub = (warp - kFirstEpi) >> 2;   // TMEM lane quarter; which 32-column chunks
@@ -309,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
         break;
       }
       ptx::tc_fence_after();
+      const Store<kPaired, Out> store(a, un.row_tile * 128 + lrow);
       const uint32_t t0 = tmem + acc * 2 * kNT + ((uint32_t)(quarter * 32) << 16);
       for (int c0 = 32 * sub; c0 < un.count; c0 += 32 * (kEpiWarps / 4)) {
         uint32_t v0[32], v1[32];
@@ -323,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
               part[(c0 + i) * 256 + 128 + lrow] = __uint_as_float(v1[i]);
             }
         } else {
+          Out* p = store.base + (un.row0 + c0) * store.ld;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c0 + i < un.count)
-              store_pair(a, un.row0 + c0 + i, un.row_tile * 128 + lrow, __uint_as_float(v0[i]), __uint_as_float(v1[i]));
+          for (int i = 0; i < 32; ++i, p += store.ld)
+            if (c0 + i < un.count) store(p, __uint_as_float(v0[i]), __uint_as_float(v1[i]));
         }
       }
       ptx::tc_fence_before();
@@ -343,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
       // rows rank, rank + cluster, ... of the unit, the parts added in rank order
       const Unit un = find_unit<kNT>(first, s_off, s_start, a.groups);
       const int i = tid & 127;
+      const Store<kPaired, Out> store(a, un.row_tile * 128 + i);
       for (int c = rank + cluster * (tid >> 7); c < un.count; c += cluster * (kThreads >> 7)) {
         const uint32_t at = ptx::smem_u32(sm) + (c * 256 + i) * 4;
         float v0 = 0.f, v1 = 0.f;
@@ -350,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
           v0 += ptx::ld_cluster_f32(at, r);
           v1 += ptx::ld_cluster_f32(at + 512, r);
         }
-        store_pair(a, un.row0 + c, un.row_tile * 128 + i, v0, v1);
+        store(store.base + (un.row0 + c) * store.ld, v0, v1);
       }
     }
     ptx::cluster_sync();   // no CTA leaves while its part is read
@@ -362,22 +358,32 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
   }
 }
 
-template <int kNT, int kNS, int kNAcc, bool kSplit>
-cudaError_t launch(const MxProductArgs& a, int cluster, int clusters, cudaStream_t st) {
+template <int kNT, int kNS, int kNAcc, bool kSplit, bool kPaired, typename Out>
+cudaError_t launch_as(const MxProductArgs& a, int cluster, int clusters, cudaStream_t st) {
   using C = Config<kNT, kNS, kNAcc>;
   static_assert(!kSplit || kNT * 256 * 4 <= kNS * C::kStage, "partial sums fit the ring");
-  auto* kernel = mx_product_kernel<kNT, kNS, kNAcc, kSplit>;
+  auto* kernel = mx_product_kernel<kNT, kNS, kNAcc, kSplit, kPaired, Out>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, dim3((unsigned)(clusters * cluster)), dim3(kThreads), C::kSmem, st,
                           kSplit ? cluster : 1, a, cluster);
 }
 
+template <int kNT, int kNS, int kNAcc, bool kSplit>
+cudaError_t launch(const MxProductArgs& a, int cluster, int clusters, cudaStream_t st) {
+  const bool f32 = a.out_type == kF32;
+  if (a.paired)
+    return f32 ? launch_as<kNT, kNS, kNAcc, kSplit, true, float>(a, cluster, clusters, st)
+               : launch_as<kNT, kNS, kNAcc, kSplit, true, __nv_bfloat16>(a, cluster, clusters, st);
+  return f32 ? launch_as<kNT, kNS, kNAcc, kSplit, false, float>(a, cluster, clusters, st)
+             : launch_as<kNT, kNS, kNAcc, kSplit, false, __nv_bfloat16>(a, cluster, clusters, st);
+}
+
 }  // namespace
 
 cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t st) {
   const int sms = sm_count();
-  if (a.n_rows > 1024) return launch<240, 3, 1, false>(a, 1, sms, st);
+  if (a.n_rows > 1024) return launch<112, 4, 2, false>(a, 1, sms, st);
   // at most this many units: every group of a batch this small is one tile
   const int64_t units = (int64_t)std::min(a.n_rows <= 64 ? a.groups : a.groups + a.n_rows / 64, a.n_rows) * a.row_tiles;
   int cluster = 1;
@@ -387,8 +393,7 @@ cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t st) {
 }
 
 cudaError_t mx_product_errors(unsigned* flags) {
-  cudaError_t e = cudaDeviceSynchronize();
-  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(flags, g_mx_err, sizeof(unsigned));
+  cudaError_t e = cudaMemcpyFromSymbol(flags, g_mx_err, sizeof(unsigned));
   const unsigned zero = 0;
   if (e == cudaSuccess && *flags) e = cudaMemcpyToSymbol(g_mx_err, &zero, sizeof(unsigned));
   return e;

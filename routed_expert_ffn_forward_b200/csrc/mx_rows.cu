@@ -52,68 +52,84 @@ __device__ __forceinline__ uint32_t spread_nibbles(uint32_t v) {
   return (v | (v << 4)) & 0x0F0F0F0Fu;
 }
 
-// One warp per chunk of 256 columns, eight consecutive values per lane, so a
-// run is a quad of lanes and its maximum two shuffles.
+// Eight consecutive values of a row from column c; zeros behind its end.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, int64_t ld, int rows, int cols, int kc,
+__device__ __forceinline__ void load8(const T* __restrict__ p, int c, int cols, float* v) {
+  if (kVec && c + 8 <= cols) {
+    constexpr int kWords = sizeof(T) / 2;
+    uint4 raw[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(p + c) + i);
+    const T* e = reinterpret_cast<const T*>(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_float<T>(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_float<T>(p[c + i]) : 0.f;
+  }
+}
+
+// A warp takes kU chunks of 256 columns at a time, all their loads first; eight
+// consecutive values per lane, so that a run is a quad of lanes and its
+// maximum two shuffles.  Bound by HBM (7168 x 2048 fp32: see kU in quantize).
+template <typename T, bool kVec, int kU>
+__global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, int64_t ld, uint32_t n, int cols, uint32_t kc,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                                                        __nv_bfloat16* __restrict__ values) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t n = (int64_t)rows * kc, step = (int64_t)gridDim.x * (blockDim.x >> 5);
-  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < n; w += step) {
-    const int64_t row = w / kc;
-    const int c0 = (int)(w - row * kc) * kMxChunk + lane * 8;
-    const T* p = x + row * ld + c0;
-    float v[8];
-    if (kVec && c0 + 8 <= cols) {
-      constexpr int kWords = sizeof(T) / 2;
-      uint4 raw[kWords];
+  const uint32_t step = gridDim.x * (blockDim.x >> 5) * kU;
+  for (uint32_t w0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kU; w0 < n; w0 += step) {
+    float v[kU][8];
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      const T* e = reinterpret_cast<const T*>(raw);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = to_float<T>(e[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c0 + i < cols ? to_float<T>(p[i]) : 0.f;
+    for (int u = 0; u < kU; ++u) {
+      const uint32_t w = min(w0 + u, n - 1), row = w / kc;
+      load8<T, kVec>(x + row * ld, (w - row * kc) * kMxChunk + lane * 8, cols, v[u]);
     }
-    uint32_t top = 0;   // magnitude bits order like the magnitudes, NaN above all
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int ef = (int)(top >> 23);
-    const int s = ef == 255 ? 255 : max(ef - 2, 0);
-    const float mul = __uint_as_float((uint32_t)(254 - min(s, 253)) << 23);   // 2^(127 - s)
-    float t[8];
+    for (int u = 0; u < kU; ++u) {
+      const uint32_t w = w0 + u;
+      if (w >= n) break;
+      uint32_t top = 0;   // magnitude bits order like the magnitudes, NaN above all
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = v[i] * mul;
-    const uint32_t w8 = e2m1_codes(t);
-    // lanes q and q ^ 2 of a quad hold elements j.. and 16 + j..: each writes
-    // one 32-bit word that pairs four of the lower with four of the upper
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, w8, 2);
-    const bool upper = lane & 2;
-    const uint32_t lo = upper ? other >> 16 : w8 & 0xFFFFu;
-    const uint32_t hi = upper ? w8 >> 16 : other & 0xFFFFu;
-    const int word = (lane & ~3) + 2 * (lane & 1) + (upper ? 1 : 0);
-    reinterpret_cast<uint32_t*>(codes)[w * 32 + word] = spread_nibbles(lo) | spread_nibbles(hi) << 4;
-    if ((lane & 3) == 0) scales[w * 8 + (lane >> 2)] = (uint8_t)s;
-    if (values) {
-      // 2^(s - 127); s = 0 is the subnormal 2^-127, s = 255 stands for NaN
-      const float up = s == 255 ? __uint_as_float(0x7FC00000u) : s ? __uint_as_float((uint32_t)s << 23)
-                                                                   : __uint_as_float(0x00400000u);
-      __nv_bfloat16 o[8];
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[u][i]) & 0x7FFFFFFFu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ef = (int)(top >> 23);
+      const int s = ef == 255 ? 255 : max(ef - 2, 0);
+      const float mul = __uint_as_float((uint32_t)(254 - min(s, 253)) << 23);   // 2^(127 - s)
+      float t[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = __float2bfloat16_rn(e2m1_value(w8 >> (4 * i)) * up);   // exact
-      __nv_bfloat16* q = values + row * cols + c0;
-      if (kVec && c0 + 8 <= cols && cols % 8 == 0) {
-        *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(o);
-      } else {
+      for (int i = 0; i < 8; ++i) t[i] = v[u][i] * mul;
+      const uint32_t w8 = e2m1_codes(t);
+      // lanes q and q ^ 2 of a quad hold elements j.. and 16 + j..: each writes
+      // one 32-bit word that pairs four of the lower with four of the upper
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, w8, 2);
+      const bool upper = lane & 2;
+      const uint32_t lo = upper ? other >> 16 : w8 & 0xFFFFu;
+      const uint32_t hi = upper ? w8 >> 16 : other & 0xFFFFu;
+      const int word = (lane & ~3) + 2 * (lane & 1) + (upper ? 1 : 0);
+      reinterpret_cast<uint32_t*>(codes)[(size_t)w * 32 + word] = spread_nibbles(lo) | spread_nibbles(hi) << 4;
+      if ((lane & 3) == 0) scales[(size_t)w * 8 + (lane >> 2)] = (uint8_t)s;
+      if (values) {
+        // 2^(s - 127); s = 0 is the subnormal 2^-127, s = 255 stands for NaN
+        const float up = s == 255 ? __uint_as_float(0x7FC00000u) : s ? __uint_as_float((uint32_t)s << 23)
+                                                                     : __uint_as_float(0x00400000u);
+        __nv_bfloat162 o[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c0 + i < cols) q[i] = o[i];
+        for (int i = 0; i < 4; ++i)   // exact
+          o[i] = __floats2bfloat162_rn(e2m1_value(w8 >> (8 * i)) * up, e2m1_value(w8 >> (8 * i + 4)) * up);
+        const uint32_t row = w / kc;
+        const int c0 = (w - row * kc) * kMxChunk + lane * 8;
+        __nv_bfloat16* q = values + (size_t)row * cols + c0;
+        if (kVec && c0 + 8 <= cols && cols % 8 == 0) {
+          *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c0 + i < cols) q[i] = i & 1 ? o[i >> 1].y : o[i >> 1].x;
+        }
       }
     }
   }
@@ -152,19 +168,25 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint8_t* __restrict__ c
   }
 }
 
+template <typename T, bool kVec>
+cudaError_t quantize_as(const T* x, int64_t ld, uint32_t n, int cols, uint8_t* codes, uint8_t* scales,
+                        __nv_bfloat16* values, cudaStream_t st) {
+  const uint32_t kc = mx_chunks(cols), sms = sm_count();
+  // a chunk per warp until the GPU is full of warps, then four
+  const bool many = n > sms * 64;
+  const unsigned blocks = std::min(many ? (n + 31) / 32 : (n + 7) / 8, sms * 8);
+  auto* kernel = many ? quantize_kernel<T, kVec, 4> : quantize_kernel<T, kVec, 1>;
+  return launch_dependent(kernel, dim3(blocks), dim3(256), 0, st, 1, x, ld, n, cols, kc, codes, scales, values);
+}
 template <typename T>
-cudaError_t quantize(const void* x, int64_t ld, int rows, int cols, uint8_t* codes, uint8_t* scales,
+cudaError_t quantize(const void* p, int64_t ld, int rows, int cols, uint8_t* codes, uint8_t* scales,
                      __nv_bfloat16* values, cudaStream_t st) {
-  const int kc = mx_chunks(cols);
-  const int64_t warps = (int64_t)rows * kc;
-  const unsigned blocks = (unsigned)std::min<int64_t>((warps + 7) / 8, (int64_t)sm_count() * 8);
+  const T* x = static_cast<const T*>(p);
+  const uint32_t n = (uint32_t)rows * mx_chunks(cols);
   const bool vec = (reinterpret_cast<uintptr_t>(x) % 16 == 0) && (ld * sizeof(T)) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(values) % 16 == 0;
-  if (vec)
-    return launch_dependent(quantize_kernel<T, true>, dim3(blocks), dim3(256), 0, st, 1, static_cast<const T*>(x), ld,
-                            rows, cols, kc, codes, scales, values);
-  return launch_dependent(quantize_kernel<T, false>, dim3(blocks), dim3(256), 0, st, 1, static_cast<const T*>(x), ld,
-                          rows, cols, kc, codes, scales, values);
+  return vec ? quantize_as<T, true>(x, ld, n, cols, codes, scales, values, st)
+             : quantize_as<T, false>(x, ld, n, cols, codes, scales, values, st);
 }
 
 }  // namespace

@@ -337,6 +337,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
+// Arrive on `bar` (once per thread, counted in its expected arrivals) when this
+// thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
 __device__ __forceinline__ void cp_async_wait() {
@@ -344,15 +349,25 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // ---- microscaled 4-bit MMA ---------------------------------------------------------
+// These are issued by a whole converged warp with the operands the same in
+// every lane and `on` nonzero in one lane (elect_one), so that descriptors and
+// addresses stay in uniform registers: from a single-lane branch each operand
+// has to be moved there first, about 70 cycles an instruction instead of 25.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on;
+}
 // D[tmem] (+)= A[smem desc] * B[smem desc], E2M1 codes with one E8M0 scale per
 // 32 values of K (64 values of K per instruction), scales in tensor memory.
-__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void umma_mxf4(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t sa_tmem, uint32_t sb_tmem, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate ? 1u : 0u)
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate ? 1u : 0u), "r"(on)
       : "memory");
 }
 // Instruction descriptor: E2M1 A and B (K-major), E8M0 scales, fp32 D, M x N.
@@ -365,15 +380,24 @@ __host__ __device__ __forceinline__ uint32_t umma_idesc_mxf4(int M, int N, int p
          | ((uint32_t)(M >> 7) << 27)           // M / 128
          | ((uint32_t)(2 * pair) << 29);        // A scale bytes
 }
-// 512 bytes of scales (32 rows of 16 bytes) from shared memory to four tensor
-// memory columns, the same in each of the four lane quarters.
-__device__ __forceinline__ void tmem_copy_scales(uint32_t tmem, uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);   // start address, 16-byte units
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(128 >> 4) << 32;             // stride byte offset: next 8-row group
-  d |= (uint64_t)1 << 46;                      // descriptor version (sm_100), no swizzle
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+// Shared-memory descriptor of 512 bytes of scales (32 rows of 16 bytes, no
+// swizzle, 8-row groups 128 bytes apart).
+__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+// 512 bytes of scales to four tensor memory columns, the same in each of the
+// four lane quarters.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t on, uint32_t tmem, uint64_t desc) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+               "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc), "r"(on)
+               : "memory");
+}
+// umma_commit by the lane with `on`
+__device__ __forceinline__ void umma_commit_on(uint32_t on, uint64_t* bar) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+               "r"(on)
+               : "memory");
 }
 
 // ---- thread-block clusters -------------------------------------------------------

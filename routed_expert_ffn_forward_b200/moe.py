@@ -50,7 +50,7 @@ EXPORTS = ("moe_expert_bytes", "moe_layer_create", "moe_layer_create_mixed", "mo
            "moe_check", "moe_get_stats", "moe_reset_stats", "moe_set_profiling", "moe_get_profile",
            "moe_reset_profile", "moe_route_noalloc", "moe_set_test_hooks", "moe_set_expert_parallel",
            "moe_forward_partial", "moe_combine_partials", "moe_mx_quantize", "moe_mx_image_bytes", "moe_mx_pack",
-           "moe_mx_product", "moe_mx_check", "moe_block_norm", "moe_block_norm_workspace", "moe_block_norm_grad",
+           "moe_mx_product", "moe_block_check", "moe_block_norm", "moe_block_norm_workspace", "moe_block_norm_grad",
            "moe_balance_workspace", "moe_balance_loss", "moe_balance_loss_grad", "moe_last_error")
 
 KERNELS = ("router", "topk", "permute", "gate_up", "down", "combine", "prep", "small", "forward", "fused",
@@ -139,7 +139,7 @@ def lib() -> ctypes.CDLL:
             "moe_mx_image_bytes": (ctypes.c_size_t, [_I, _I, _I]),
             "moe_mx_pack": (_I, [_P, _P, _I, _I, _I, _I, _P, _P]),
             "moe_mx_product": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _L, _P]),
-            "moe_mx_check": (_I, []),
+            "moe_block_check": (_I, []),
             "moe_block_norm": (_I, [ctypes.POINTER(moe_norm_args), _P]),
             "moe_block_norm_workspace": (ctypes.c_size_t, [_I, _I]),
             "moe_block_norm_grad": (_I, [ctypes.POINTER(moe_norm_args), ctypes.POINTER(moe_norm_grads), _P,
@@ -302,8 +302,8 @@ def moe_mx_product(codes: int, scales: int, n_x: int, image: int, n_mats: int, r
                                 index or None, n_rows, out, out_type, ld, stream or None))
 
 
-def moe_mx_check() -> None:
-    _check(lib().moe_mx_check())
+def moe_block_check() -> None:
+    _check(lib().moe_block_check())
 
 
 def moe_block_norm(args: moe_norm_args, stream: int | None = None) -> None:

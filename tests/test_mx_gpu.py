@@ -23,7 +23,7 @@ def gpu():
     build.build()
     yield
     from routed_expert_ffn_forward_b200 import block
-    block.mx_check()
+    block.check()
 
 
 from routed_expert_ffn_forward_b200 import block  # noqa: E402
