@@ -261,6 +261,28 @@ moe_status moe_forward(moe_layer_t layer, const void* x, void* out, int T, void*
 moe_status moe_forward_routed(moe_layer_t layer, const void* x, void* out, int T,
                               const int32_t* forced_ids, void* stream);
 
+/* The layer with its experts in MXFP4 and its products on the block-scaled
+ * tensor cores, for batches (moe_forward runs MXFP4 layers one token per
+ * launch): gate_up and down are images of moe_mx_pack for all E + S experts,
+ * gate_up of n_mats = E + S matrices [2 inter, hidden], gate rows first, with
+ * paired = 1, down of [hidden, inter] with paired = 0; device memory, 16-byte
+ * aligned, borrowed until the layer is destroyed or given others.  The layer
+ * needs no moe_set_experts for it.  Errors: INVALID_ARG, UNSUPPORTED (E + S >
+ * 1024). */
+moe_status moe_set_mx_experts(moe_layer_t layer, const void* gate_up, const void* down);
+
+/* moe_forward over the experts of moe_set_mx_experts, any T: the router, top-k,
+ * permutation and combine of the prefill path, with x and the SwiGLU output
+ * (rounded to bf16) in MXFP4 as moe_mx_quantize gives it and fp32 sums.  Both
+ * operands are 4-bit, so the output differs from moe_forward's (which keeps 16
+ * bits of the activations) by the activations' rounding to E2M1, up to 1/6 of a
+ * value.  Never waits for the GPU except as moe_forward's first call at a T;
+ * can be captured in a CUDA graph after that.  Counts as a prefill call.
+ * Errors: as moe_forward; NOT_READY without moe_set_mx_experts, UNSUPPORTED
+ * with expert parallelism.  moe_get_routing and moe_get_logits give its
+ * routing; moe_block_check reports a product that gave up waiting. */
+moe_status moe_forward_mx(moe_layer_t layer, const void* x, void* out, int T, void* stream);
+
 /* Forward on HOST buffers: x (host, bf16 [T, H]) in, moe_forward, out (host,
  * bf16 [T, H]) back, all on `stream`; returns once the work is enqueued
  * (synchronise the stream before reading out).  With T <= 4 and pinned

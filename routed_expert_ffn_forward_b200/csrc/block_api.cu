@@ -52,6 +52,8 @@ moe_status launched(cudaError_t e, unsigned launches, const char* what) {
 bool known_type(int t) { return t == kF32 || t == kF16 || t == kBF16; }
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// 1024 matrices of 2^20 x 65536 are 2^30 blocks, and a product's units at most
+// (1024 + 2^24 / 64) x 4096 < 2^31: both fit an int
 constexpr int kMaxMxCols = 1 << 16, kMaxMxRows = 1 << 20, kMaxMats = 1024, kMaxRows = 1 << 24;
 
 bool mx_shape(int n_mats, int rows, int cols) {
@@ -143,8 +145,6 @@ moe_status moe_mx_pack(const uint8_t* codes, const uint8_t* scales, int n_mats, 
   clear_error();
   if (!mx_shape(n_mats, rows, cols) || (paired && rows % 2))
     return fail(MOE_ERR_INVALID_ARG, "n_mats=%d rows=%d cols=%d paired=%d", n_mats, rows, cols, paired);
-  if ((long long)n_mats * mx_row_tiles(rows) * mx_chunks(cols) > 0x7FFFFFFFll)
-    return fail(MOE_ERR_UNSUPPORTED, "n_mats=%d rows=%d cols=%d: too many blocks", n_mats, rows, cols);
   if (!codes || !scales || !image) return fail(MOE_ERR_INVALID_ARG, "null pointer");
   if (!aligned(codes, 16) || !aligned(scales, 8) || !aligned(image, 16))
     return fail(MOE_ERR_INVALID_ARG, "codes and image must be aligned to 16 bytes, scales to 8");
@@ -165,8 +165,6 @@ moe_status moe_mx_product(const uint8_t* codes, const uint8_t* scales, int n_x, 
     return fail(MOE_ERR_UNSUPPORTED, "output type %d (supported: F32=0, BF16=30)", (int)out_type);
   if (!offsets && n_mats != 1) return fail(MOE_ERR_INVALID_ARG, "%d matrices need offsets", n_mats);
   if (!index && n_rows > n_x) return fail(MOE_ERR_INVALID_ARG, "%d rows of %d without an index", n_rows, n_x);
-  if (((long long)n_mats + n_rows / 64 + 1) * mx_row_tiles(rows) > 0x7FFFFFFFll)
-    return fail(MOE_ERR_UNSUPPORTED, "n_rows=%d rows=%d: too many tiles", n_rows, rows);
   if (n_rows == 0) return MOE_OK;
   if (!codes || !scales || !image || !out) return fail(MOE_ERR_INVALID_ARG, "null pointer");
   const size_t size = type_bytes(out_type);
@@ -179,6 +177,7 @@ moe_status moe_mx_product(const uint8_t* codes, const uint8_t* scales, int n_x, 
   a.image = static_cast<const uint8_t*>(image);
   a.offsets = offsets;
   a.index = index;
+  a.index_div = 1;
   a.out = out;
   a.ld = ld;
   a.n_x = n_x;

@@ -67,10 +67,10 @@ struct MxProductArgs {
   const uint8_t* scales;   // [n_x, 8 * kc]
   const uint8_t* image;    // [groups][row tiles][kc][kMxBlockBytes]
   const int* offsets;      // [groups + 1] or null (one group of all rows)
-  const int* index;        // [n_rows] or null (row r is row r of x)
+  const int* index;        // [n_rows], index[r] / index_div is a row of x; or null (row r is row r of x)
   void* out;               // [n_rows, ld]
   int64_t ld;
-  int n_x, n_rows, groups, kc, row_tiles, features, out_type;
+  int index_div, n_x, n_rows, groups, kc, row_tiles, features, out_type;
   bool paired, wide_store;
 };
 cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t st);

@@ -220,6 +220,7 @@ struct moe_layer {
   cudaEvent_t done = nullptr;           // recorded on the stream at the end of every forward
   bool done_rec = false;
   int last_T = 0;
+  const uint8_t *mx_gate_up = nullptr, *mx_down = nullptr;   // borrowed packed images (moe_set_mx_experts)
   CUtensorMap x16_map{}, h16_map{};     // B operands of the prefill GEMMs (over the scratch)
 };
 
@@ -890,6 +891,113 @@ moe_status forward_impl(moe_layer* L, const void* x, void* out, int T, const int
   return MOE_OK;
 }
 
+// The forward with its projections as MXFP4 products: router, top-k and
+// permutation as on the prefill path, the activations and the SwiGLU output
+// quantised row by row, two grouped products, the combine.  Its intermediates
+// lie in scratch that the other paths use for theirs.
+moe_status forward_mx_impl(moe_layer* L, const void* x, void* out, int T, cudaStream_t st) {
+  NvtxRange nv("moe.forward MXFP4");
+  if (!L) return fail(MOE_ERR_INVALID_ARG, "null layer");
+  if (T < 0 || T > kMaxTokens) return fail(MOE_ERR_INVALID_ARG, "T=%d outside 0..%d", T, kMaxTokens);
+  if (T > 0 && (!x || !out)) return fail(MOE_ERR_INVALID_ARG, "null x or out");
+  if (!L->router_set) return fail(MOE_ERR_NOT_READY, "router not set");
+  if (!L->mx_gate_up) return fail(MOE_ERR_NOT_READY, "MXFP4 experts not set");
+  if (L->ep_world != 1) return fail(MOE_ERR_UNSUPPORTED, "expert parallelism with MXFP4 products");
+  MOE_TRY(check_device(L));
+  if (T == 0) return MOE_OK;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & 15)
+    return fail(MOE_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
+  MOE_TRY(ensure_scratch(L, T, st));
+  const Shape& s = L->s;
+  const Work& wk = L->wk;
+  const int kS = s.k + s.S, P = T * kS;
+  ProfRec pr{};
+  bool prof;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    prof = g_profiling;
+    if (prof)
+      for (int i = 0; i < 2 * kProfRanges; ++i) pr.ev[i] = prof_event();
+  }
+  int n_launch = 0;
+#define MOE_KERNEL(k_id, call)                                \
+  do {                                                        \
+    if (prof) CUDA_TRY(cudaEventRecord(pr.ev[2 * pr.n], st)); \
+    CUDA_TRY(call);                                           \
+    if (prof) {                                               \
+      CUDA_TRY(cudaEventRecord(pr.ev[2 * pr.n + 1], st));     \
+      pr.kid[pr.n++] = (k_id);                                \
+    }                                                         \
+    ++n_launch;                                               \
+  } while (0)
+  CUtensorMap xmap;
+  if (encode_sw128_16(&xmap, x, true, (size_t)T, s.H, 128) != cudaSuccess)
+    return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for x");
+  RouterGemmArgs rg{};
+  rg.T = T;
+  rg.E = s.E;
+  rg.nsplit = router_gemm_splits(T, s.E, s.H, s.n_sm);
+  rg.nk_split = s.H / 64 / rg.nsplit;
+  rg.part = wk.rpart;
+  rg.split_stride = (size_t)T * s.E;
+  rg.err = wk.err;
+  MOE_KERNEL(MOE_K_ROUTER, launch_router_gemm(xmap, L->wp_map, rg, st));
+  MOE_KERNEL(MOE_K_TOPK, launch_topk(wk.logits, T, s.E, s.k, (int)L->gating, nullptr, wk.ids, wk.w, st, wk.rpart,
+                                     rg.nsplit, rg.split_stride, L->d_b));
+  MOE_KERNEL(MOE_K_PERMUTE, launch_permute(wk.ids, T, s, wk, st));
+  // codes and scales of x in the fixed-point planes of the decode path
+  // (2 bytes a value, 17/32 used), those of h in theirs; h as bf16 in h16
+  uint8_t *xc = reinterpret_cast<uint8_t*>(wk.xq), *hc = reinterpret_cast<uint8_t*>(wk.hq);
+  uint8_t *xs = xc + (size_t)T * (s.H / 2), *hs = hc + (size_t)P * (s.I_pad / 2);
+  MOE_KERNEL(MOE_K_PREP, launch_mx_quantize(x, kBF16, s.H, T, s.H, xc, xs, nullptr, st));
+  MxProductArgs a{};
+  a.codes = xc;
+  a.scales = xs;
+  a.image = L->mx_gate_up;
+  a.offsets = wk.offsets;
+  a.index = wk.perm;      // row r is pair t * (k + S) + j: token t's row of x
+  a.index_div = kS;
+  a.out = wk.h16;
+  a.ld = s.I;
+  a.n_x = T;
+  a.n_rows = P;
+  a.groups = s.E + s.S;
+  a.kc = s.nbh;
+  a.row_tiles = mx_row_tiles(2 * s.I);
+  a.features = s.I;
+  a.out_type = kBF16;
+  a.paired = true;
+  MOE_KERNEL(MOE_K_GATE_UP, launch_mx_product(a, st));
+  MOE_KERNEL(MOE_K_PREP, launch_mx_quantize(wk.h16, kBF16, s.I, P, s.I, hc, hs, nullptr, st));
+  a.codes = hc;
+  a.scales = hs;
+  a.image = L->mx_down;
+  a.index = nullptr;
+  a.index_div = 1;
+  a.out = wk.y;
+  a.ld = s.H;
+  a.n_x = P;
+  a.kc = s.nbi;
+  a.row_tiles = mx_row_tiles(s.H);
+  a.features = s.H;
+  a.out_type = kF32;
+  a.paired = false;
+  a.wide_store = true;
+  MOE_KERNEL(MOE_K_DOWN, launch_mx_product(a, st));
+  MOE_KERNEL(MOE_K_COMBINE, launch_combine(wk, T, s, static_cast<__nv_bfloat16*>(out), st, true));
+#undef MOE_KERNEL
+  CUDA_TRY(cudaEventRecord(L->done, st));
+  L->done_rec = true;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (prof) g_prof_pending.push_back(pr);
+  g_stats.launches += (uint64_t)n_launch;
+  g_stats.forwards++;
+  g_stats.tokens += (uint64_t)T;
+  g_stats.prefill_calls++;
+  L->last_T = T;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1242,6 +1350,23 @@ moe_status moe_forward_host(moe_layer_t L, const void* x_host, void* out_host, i
   MOE_TRY(forward_impl(L, L->xbuf, o_dev ? o_dev : L->obuf, T, nullptr, st));
   if (!o_dev) CUDA_TRY(cudaMemcpyAsync(out_host, L->obuf, bytes, cudaMemcpyDeviceToHost, st));
   return MOE_OK;
+}
+
+moe_status moe_set_mx_experts(moe_layer_t L, const void* gate_up, const void* down) {
+  g_err.clear();
+  if (!L || !gate_up || !down) return fail(MOE_ERR_INVALID_ARG, "null argument");
+  if ((reinterpret_cast<uintptr_t>(gate_up) | reinterpret_cast<uintptr_t>(down)) & 15)
+    return fail(MOE_ERR_INVALID_ARG, "the images must be 16-byte aligned");
+  if (L->s.E + L->s.S > 1024)
+    return fail(MOE_ERR_UNSUPPORTED, "%d experts: a product has at most 1024 matrices", L->s.E + L->s.S);
+  L->mx_gate_up = static_cast<const uint8_t*>(gate_up);
+  L->mx_down = static_cast<const uint8_t*>(down);
+  return MOE_OK;
+}
+
+moe_status moe_forward_mx(moe_layer_t L, const void* x, void* out, int T, void* stream) {
+  g_err.clear();
+  return forward_mx_impl(L, x, out, T, static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_get_routing(moe_layer_t L, int32_t* ids, float* weights, void* stream) {

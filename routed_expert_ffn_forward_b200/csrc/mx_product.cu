@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
       // and the scales of rows tid + 128 j; -1: not a row of x, read as zeros
       auto row_of = [&](int r) {
         if (r >= un.count) return -2;
-        const int src = a.index ? __ldg(a.index + un.row0 + r) : un.row0 + r;
+        int src = a.index ? __ldg(a.index + un.row0 + r) : un.row0 + r;
+        if (a.index_div > 1) src /= a.index_div;
         return (unsigned)src < (unsigned)a.n_x ? src : -1;
       };
       int rows[kNT / 16], srows[C::kScaleTiles];

@@ -13,7 +13,7 @@ from typing import Callable, Optional
 import numpy as np
 import torch
 
-from . import moe, synth
+from . import block, moe, synth
 
 
 class MoELayer:
@@ -29,9 +29,12 @@ class MoELayer:
         self.down_bytes = hidden * synth.row_bytes(quants[2], inter)
         self.expert_bytes = 2 * self.gate_bytes + self.down_bytes   # host (GGUF) bytes
         self.host: Optional[torch.Tensor] = None
+        self.gating = moe.MOE_GATE_SIGMOID_RENORM
+        self.mx = None                       # (gate_up, down) packed weights of forward_mx
 
     # ------------------------------------------------------------ setup
     def set_router(self, W: np.ndarray, b: Optional[np.ndarray], gating: int) -> None:
+        self.gating = gating
         W = np.ascontiguousarray(W, dtype=np.float32)
         bb = None if b is None else np.ascontiguousarray(b, dtype=np.float32)
         moe.moe_set_router(self.handle, W.ctypes.data, None if bb is None else bb.ctypes.data, gating)
@@ -83,6 +86,68 @@ class MoELayer:
         s = stream if stream is not None else torch.cuda.current_stream().cuda_stream
         moe.moe_forward_routed(self.handle, x.data_ptr(), out.data_ptr(), T, ids.ctypes.data, s)
         return out
+
+    # ------------------------------------------------------------ MXFP4 products
+    def set_mx_experts(self, gate_up: block.MXWeights, down: block.MXWeights) -> None:
+        """Packed MXFP4 weights of all E + S experts for ``forward_mx``: gate_up
+        [2 inter, hidden] paired (gate rows first), down [hidden, inter]."""
+        n = self.E + self.S
+        want = ((n, 2 * self.I, self.H, True), (n, self.H, self.I, False))
+        for name, w, shape in zip(("gate_up", "down"), (gate_up, down), want):
+            if (w.n_mats, w.rows, w.cols, w.paired) != shape:
+                raise ValueError(f"{name} must be {shape} (n_mats, rows, cols, paired), "
+                                 f"not {(w.n_mats, w.rows, w.cols, w.paired)}")
+        moe.moe_set_mx_experts(self.handle, gate_up.image.data_ptr(), down.image.data_ptr())
+        self.mx = (gate_up, down)            # the library borrows the images
+
+    def mx_experts_from_host(self) -> None:
+        """Pack the pinned store's MXFP4 experts (a layer of MXFP4 weights) for ``forward_mx``."""
+        if self.quants != (moe.MOE_MXFP4,) * 3 or self.host is None:
+            raise ValueError("the layer has no MXFP4 weights in its pinned store")
+        gate_up, down = [], []
+        for e in range(self.E + self.S):
+            g, u, d = (torch.from_numpy(v) for v in self.expert_views(e))
+            gate_up.append(torch.cat([g, u]).cuda())
+            down.append(d.cuda())
+        self.set_mx_experts(block.mx_pack(block.mx_from_blocks(torch.stack(gate_up), self.H), paired=True),
+                            block.mx_pack(block.mx_from_blocks(torch.stack(down), self.I)))
+
+    def forward_mx(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The layer's forward over the MXFP4 products (see ``moe_forward_mx``)."""
+        T = x.shape[0]
+        if out is None:
+            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device)
+        s = stream if stream is not None else torch.cuda.current_stream().cuda_stream
+        moe.moe_forward_mx(self.handle, x.data_ptr(), out.data_ptr(), T, s)
+        return out
+
+    # ------------------------------------------------------------ the block around the layer
+    def forward_block(self, h: torch.Tensor, pre: torch.Tensor, post: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, scale: float = 1.0, next_pre: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, mx: bool = False):
+        """A whole MoE block on the residual stream h (bf16 [T, H]), on the current
+        stream: the norm before (weights pre), the layer (``forward``, or
+        ``forward_mx``), and in one pass the norm after (post; ones if None) with
+        gate, scale and residual and the next block's norm before (next_pre).
+        Returns (the new h, the next block's input or None).  gate and weights as
+        in ``block.block_norm``; no gradients."""
+        if h.dtype != torch.bfloat16 or h.dim() != 2 or h.shape[1] != self.H:
+            raise ValueError(f"h must be bfloat16 [T, {self.H}], not {h.dtype} {tuple(h.shape)}")
+        _, x, _ = block.block_norm_forward(h, None, None, None, 1.0, pre, eps)
+        y = self.forward_mx(x) if mx else self.forward(x)
+        if post is None:
+            post = torch.ones_like(pre)
+        new, nxt, _ = block.block_norm_forward(h, y, post, gate, scale, next_pre, eps)
+        return new, nxt
+
+    def balance_loss(self, T: int, coef: float, offsets: Optional[torch.Tensor] = None,
+                     mask: Optional[torch.Tensor] = None):
+        """Balance loss of the last forward's routing (T tokens), its per-expert
+        counts and the gradient of the router's logits: (loss, counts [seqs, E],
+        d_logits [T, E]); see ``block.balance_loss``."""
+        logits = self.logits(T)
+        loss, counts, slope = block.balance_loss_forward(logits, self.routing(T)[0], coef, self.gating, offsets, mask)
+        return loss, counts, block.balance_loss_backward(None, slope, logits, self.gating, offsets, mask)
 
     def routing(self, T: int):
         ids = torch.empty((T, self.k), dtype=torch.int32, device="cuda")

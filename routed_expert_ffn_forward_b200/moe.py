@@ -50,7 +50,7 @@ EXPORTS = ("moe_expert_bytes", "moe_layer_create", "moe_layer_create_mixed", "mo
            "moe_check", "moe_get_stats", "moe_reset_stats", "moe_set_profiling", "moe_get_profile",
            "moe_reset_profile", "moe_route_noalloc", "moe_set_test_hooks", "moe_set_expert_parallel",
            "moe_forward_partial", "moe_combine_partials", "moe_mx_quantize", "moe_mx_image_bytes", "moe_mx_pack",
-           "moe_mx_product", "moe_block_check", "moe_block_norm", "moe_block_norm_workspace", "moe_block_norm_grad",
+           "moe_mx_product", "moe_set_mx_experts", "moe_forward_mx", "moe_block_check", "moe_block_norm", "moe_block_norm_workspace", "moe_block_norm_grad",
            "moe_balance_workspace", "moe_balance_loss", "moe_balance_loss_grad", "moe_last_error")
 
 KERNELS = ("router", "topk", "permute", "gate_up", "down", "combine", "prep", "small", "forward", "fused",
@@ -139,6 +139,8 @@ def lib() -> ctypes.CDLL:
             "moe_mx_image_bytes": (ctypes.c_size_t, [_I, _I, _I]),
             "moe_mx_pack": (_I, [_P, _P, _I, _I, _I, _I, _P, _P]),
             "moe_mx_product": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _L, _P]),
+            "moe_set_mx_experts": (_I, [_P, _P, _P]),
+            "moe_forward_mx": (_I, [_P, _P, _P, _I, _P]),
             "moe_block_check": (_I, []),
             "moe_block_norm": (_I, [ctypes.POINTER(moe_norm_args), _P]),
             "moe_block_norm_workspace": (ctypes.c_size_t, [_I, _I]),
@@ -300,6 +302,14 @@ def moe_mx_product(codes: int, scales: int, n_x: int, image: int, n_mats: int, r
                    stream: int | None = None) -> None:
     _check(lib().moe_mx_product(codes, scales, n_x, image, n_mats, rows, cols, 1 if paired else 0, offsets or None,
                                 index or None, n_rows, out, out_type, ld, stream or None))
+
+
+def moe_set_mx_experts(layer: int, gate_up: int, down: int) -> None:
+    _check(lib().moe_set_mx_experts(layer, gate_up, down))
+
+
+def moe_forward_mx(layer: int, x: int, out: int, T: int, stream: int | None = None) -> None:
+    _check(lib().moe_forward_mx(layer, x, out, T, stream or None))
 
 
 def moe_block_check() -> None:
