@@ -162,6 +162,11 @@ PRODUCTS = [
     (5, [300, 0, 7, 241, 240], 333, 288, False),
     (5, [1, 480, 0, 481, 40], 258, 544, True),
     (40, None, 256, 256, False),
+    # many rows: CTA pairs, an odd number of row tiles, tiles of 240 and of a few rows
+    (3, [500, 0, 700], 700, 320, False),
+    (4, [1, 1100, 240, 17], 1290, 288, True),
+    (6, [0, 241, 112, 113, 480, 128], 513, 1500, False),
+    (2, [900, 300], 200, 256, True),
 ]
 
 
