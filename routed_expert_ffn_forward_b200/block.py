@@ -9,6 +9,13 @@ device, does not wait for the GPU and can be captured in a CUDA graph.
 
 Tensors that do not fit raise ValueError, refused calls of the library
 ``moe.MoEError``.
+
+``block_norm`` and ``balance_loss`` are differentiable (once); the *_forward and
+*_backward functions below them are the same operators without autograd.  A
+backward pass can be captured in a CUDA graph through those, or through
+``torch.autograd.grad``; with ``Tensor.backward`` it must not be while an eager
+graph of the same leaves is alive, as for any operator of torch (the leaves'
+gradients are then accumulated on the eager graph's stream, outside the capture).
 """
 from __future__ import annotations
 
@@ -20,6 +27,7 @@ from . import moe
 
 TYPES = {torch.float32: moe.MOE_F32, torch.float16: moe.MOE_F16, torch.bfloat16: moe.MOE_BF16}
 MX_CHUNK = 256   # columns per chunk of an MXFP4 row (128 code bytes, 8 scale bytes)
+MX_BLOCK = 34816  # bytes of 256 weight rows x 256 columns in a packed image
 
 
 # A call on a few tokens takes the GPU two or three microseconds, less than the
@@ -199,8 +207,9 @@ def mx_product(x: MXRows, weights: MXWeights, offsets: Optional[torch.Tensor] = 
     c = _like(codes, "codes", torch.uint8, (n_x, 128 * kc), dev)
     s = _like(scales, "scales", torch.uint8, (n_x, 8 * kc), dev)
     w = weights.image.data_ptr()
-    if weights.image.device != dev:
-        raise ValueError(f"the weights are on {weights.image.device}, the rows on {dev}")
+    if weights.image.device != dev or weights.image.numel() != weights.n_mats * -(-weights.rows // 256) * kc * MX_BLOCK:
+        raise ValueError(f"the weights' image is {weights.image.numel()} bytes on {weights.image.device}, "
+                         f"not that of {weights.n_mats} matrices {weights.rows} x {cols} on {dev}")
     off = _like(offsets, "offsets", torch.int32, (weights.n_mats + 1,), dev)
     ix = _like(index, "index", torch.int32, (n_rows,), dev)
     if out is None:

@@ -128,56 +128,125 @@ struct Packed<__nv_bfloat16> {
   }
 };
 
-// The eight columns of vector k of this thread: consecutive ones with 16-byte
-// accesses (kWide: cols a multiple of 8, everything aligned), else every
-// threads-th, so that a warp's single accesses stay side by side.
-template <bool kWide>
+// How rows are accessed.  kAligned: cols and row strides multiples of 8, bases
+// aligned to 16 bytes.  kShifted: rows at any offset, read from a copy in
+// shared memory at the same offset from a 16-byte boundary and stored in whole
+// 16-byte words, both by shifting across word borders.  kStrided: single accesses.
+enum Access { kStrided, kAligned, kShifted };
+
+// The eight columns of vector k of this thread: consecutive ones, or with
+// kStrided every threads-th, so that a warp's single accesses stay side by side.
+template <Access kA>
 __device__ __forceinline__ int column(int threads, int k, int i) {
-  return kWide ? (threadIdx.x + k * threads) * kVec + i : threadIdx.x + (k * kVec + i) * threads;
+  return kA != kStrided ? (threadIdx.x + k * threads) * kVec + i : threadIdx.x + (k * kVec + i) * threads;
 }
 // A row's columns and the threads that share them.
 struct Span {
   int cols, threads;
 };
+// kN words of a stream of kN + 4 words from byte `shift` (0..15) on
+template <int kN>
+__device__ __forceinline__ void shifted_words(const uint32_t* w, uint32_t shift, uint32_t* out) {
+  const bool two = shift & 8, one = shift & 4;
+  const uint32_t bits = (shift & 3) * 8;
+  uint32_t t[kN + 2], u[kN + 1];
+#pragma unroll
+  for (int i = 0; i < kN + 2; ++i) t[i] = two ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < kN + 1; ++i) u[i] = one ? t[i + 1] : t[i];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) out[i] = __funnelshift_r(u[i], u[i + 1], bits);
+}
 // Vector k of a row; zeros behind its end.  Single 16-bit values are loaded
 // plainly: __ldg of a half type is an asm statement that is not volatile, so
 // the compiler may run it ahead of the test that guards it, with a pointer
 // that is not valid.
-template <typename T, bool kWide, bool kShared>
+template <typename T, Access kA, bool kShared>
 __device__ __forceinline__ V8 load8(const T* row, int k, const Span& sp) {
   V8 v = all8(0.f);
-  if (kWide) {
-    const int c = column<true>(sp.threads, k, 0);
-    if (c < sp.cols) {
-      uint4 raw[Packed<T>::kWords];
-      const uint4* p = reinterpret_cast<const uint4*>(row + c);
-#pragma unroll
-      for (int i = 0; i < Packed<T>::kWords; ++i) raw[i] = kShared ? p[i] : __ldg(p + i);
-      v = Packed<T>::unpack(raw);
-    }
-  } else {
+  constexpr int kWords = Packed<T>::kWords;
+  if (kA == kStrided) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int c = column<false>(sp.threads, k, i);
+      const int c = column<kStrided>(sp.threads, k, i);
       if (c < sp.cols) v.set(i, up(row[c]));
     }
+    return v;
+  }
+  const int c = column<kAligned>(sp.threads, k, 0);
+  if (c >= sp.cols) return v;
+  if (kA == kAligned) {
+    uint4 raw[kWords];
+    const uint4* p = reinterpret_cast<const uint4*>(row + c);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) raw[i] = kShared ? p[i] : __ldg(p + i);
+    return Packed<T>::unpack(raw);
+  }
+  // shared memory: the words that hold the vector and one more
+  const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;
+  const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(row + c) - shift);
+  uint4 raw[kWords + 1], out[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords + 1; ++i) raw[i] = p[i];
+  shifted_words<4 * kWords>(reinterpret_cast<const uint32_t*>(raw), shift, reinterpret_cast<uint32_t*>(out));
+  v = Packed<T>::unpack(out);
+  if (c + kVec > sp.cols) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (c + i >= sp.cols) v.set(i, 0.f);
   }
   return v;
 }
-template <typename T, bool kWide>
+template <typename T, Access kA>
 __device__ __forceinline__ void store8(T* row, int k, const Span& sp, const V8& v) {
-  if (kWide) {
-    const int c = column<true>(sp.threads, k, 0);
-    if (c >= sp.cols) return;
-    uint4 raw[Packed<T>::kWords];
-    Packed<T>::pack(v, raw);
-#pragma unroll
-    for (int i = 0; i < Packed<T>::kWords; ++i) reinterpret_cast<uint4*>(row + c)[i] = raw[i];
-  } else {
+  constexpr int kWords = Packed<T>::kWords;
+  if (kA == kStrided) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int c = column<false>(sp.threads, k, i);
+      const int c = column<kStrided>(sp.threads, k, i);
       if (c < sp.cols) row[c] = down<T>(v.get(i));
+    }
+    return;
+  }
+  const int c = column<kAligned>(sp.threads, k, 0);
+  if (kA == kAligned) {
+    if (c >= sp.cols) return;
+    uint4 raw[kWords];
+    Packed<T>::pack(v, raw);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4*>(row + c)[i] = raw[i];
+    return;
+  }
+  // The whole warp: a lane stores the 16-byte words that end in its vector, with
+  // the last bytes of the lane before; what no lane can store whole (a warp's
+  // first and last bytes, a row's last vector) goes value by value.
+  const int lane = threadIdx.x & 31;
+  uint4 raw[kWords + 1], out[kWords];   // the previous lane's last word, then this vector
+  Packed<T>::pack(v, raw + 1);
+  const uint32_t* last = reinterpret_cast<const uint32_t*>(raw + kWords);
+  uint32_t* before = reinterpret_cast<uint32_t*>(raw);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) before[i] = __shfl_up_sync(0xffffffffu, last[i], 1);
+  if (c >= sp.cols) return;
+  const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;
+  const bool full = c + kVec <= sp.cols, next = lane < 31 && c + 2 * kVec <= sp.cols;
+  uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(row + c) - shift);
+  if (shift == 0) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) out[i] = raw[1 + i];
+  } else {
+    shifted_words<4 * kWords>(reinterpret_cast<const uint32_t*>(raw), 16 - shift, reinterpret_cast<uint32_t*>(out));
+  }
+  const bool merge = full && (lane > 0 || shift == 0);   // the first word is whole
+#pragma unroll
+  for (int i = 0; i < kWords; ++i)
+    if (full && (i > 0 || merge)) q[i] = out[i];
+  const int head = shift ? (16 - (int)shift) / (int)sizeof(T) : kVec, tail = kVec - (int)shift / (int)sizeof(T);
+  if (!merge || !next) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const bool mine = full ? (!merge && i < head) || (!next && i >= tail) : c + i < sp.cols;
+      if (mine) row[c + i] = down<T>(v.get(i));
     }
   }
 }
@@ -237,11 +306,16 @@ struct Weights {
 };
 
 // v times scale and the gate
-template <typename T, typename W, bool kWide, bool kShared>
+// Weights in shared memory are aligned where the rows are shifted.
+template <typename W, Access kA, bool kShared>
+__device__ __forceinline__ V8 weight8(const W* w, int k, const Span& sp) {
+  return load8<W, kA == kShifted ? kAligned : kA, kShared>(w, k, sp);
+}
+template <typename T, typename W, Access kA, bool kShared>
 __device__ __forceinline__ V8 gated(const NormArgs& a, const V8& v, float scale, const Row<T>& r, const Weights<W>& w, int k,
                                     const Span& sp) {
-  if (a.gate_kind == kGateFull) return v * (load8<T, kWide, kShared>(r.gate, k, sp) * scale);
-  if (a.gate_kind == kGateFeature) return v * (load8<W, kWide, kShared>(w.gate, k, sp) * scale);
+  if (a.gate_kind == kGateFull) return v * (load8<T, kA, kShared>(r.gate, k, sp) * scale);
+  if (a.gate_kind == kGateFeature) return v * (weight8<W, kA, kShared>(w.gate, k, sp) * scale);
   return v * scale;
 }
 // scale, times a token's gate
@@ -253,7 +327,7 @@ __device__ __forceinline__ float token_scale(const NormArgs& a, const Row<T>& r)
 }
 
 // One row forward.  `read` is called by every thread once it has read the row.
-template <typename T, typename W, int kV, bool kWide, bool kShared, typename Read>
+template <typename T, typename W, int kV, Access kA, bool kShared, typename Read>
 __device__ __forceinline__ void row_forward(const NormArgs& a, int64_t row, const Row<T>& in, const Weights<W>& wt,
                                             BlockSum& sum, Read read) {
   const float inv = 1.f / (float)a.cols;
@@ -264,7 +338,7 @@ __device__ __forceinline__ void row_forward(const NormArgs& a, int64_t row, cons
     float2 q = both(0.f);
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      y[k] = load8<T, kWide, kShared>(in.y, k, sp);
+      y[k] = load8<T, kA, kShared>(in.y, k, sp);
       dot8(y[k], y[k], q);
     }
     const float sg = token_scale(a, in);
@@ -272,13 +346,13 @@ __device__ __forceinline__ void row_forward(const NormArgs& a, int64_t row, cons
     if (threadIdx.x == 0 && a.stats) a.stats[2 * row] = r;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      const V8 z = y[k] * load8<W, kWide, kShared>(wt.post, k, sp);
-      o[k] = fma8(gated<T, W, kWide, kShared>(a, z, sg, in, wt, k, sp), r, load8<T, kWide, kShared>(in.h, k, sp));
-      store8<T, kWide>(static_cast<T*>(a.out) + row * a.ld_out, k, sp, o[k]);
+      const V8 z = y[k] * weight8<W, kA, kShared>(wt.post, k, sp);
+      o[k] = fma8(gated<T, W, kA, kShared>(a, z, sg, in, wt, k, sp), r, load8<T, kA, kShared>(in.h, k, sp));
+      store8<T, kA>(static_cast<T*>(a.out) + row * a.ld_out, k, sp, o[k]);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < kV; ++k) o[k] = load8<T, kWide, kShared>(in.h, k, sp);
+    for (int k = 0; k < kV; ++k) o[k] = load8<T, kA, kShared>(in.h, k, sp);
   }
   read();
   if (a.pre) {
@@ -289,8 +363,8 @@ __device__ __forceinline__ void row_forward(const NormArgs& a, int64_t row, cons
     if (threadIdx.x == 0 && a.stats) a.stats[2 * row + 1] = r;
 #pragma unroll
     for (int k = 0; k < kV; ++k)
-      store8<T, kWide>(static_cast<T*>(a.next) + row * a.ld_next, k, sp,
-                       o[k] * r * load8<W, kWide, kShared>(wt.pre, k, sp));
+      store8<T, kA>(static_cast<T*>(a.next) + row * a.ld_next, k, sp,
+                       o[k] * r * weight8<W, kA, kShared>(wt.pre, k, sp));
   }
 }
 
@@ -303,7 +377,7 @@ struct ColumnSums {
 };
 
 // One row backward; `read` as above.
-template <typename T, typename W, int kV, bool kWide, bool kShared, typename Read>
+template <typename T, typename W, int kV, Access kA, bool kShared, typename Read>
 __device__ __forceinline__ void row_backward(const NormGradArgs& a, int64_t row, float2 stats, const Row<T>& in,
                                              const Weights<W>& wt, BlockSum& sum, ColumnSums<kV>& s, Read read) {
   const NormArgs& f = a.f;
@@ -316,43 +390,43 @@ __device__ __forceinline__ void row_backward(const NormGradArgs& a, int64_t row,
     float2 q = both(0.f);
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      o[k] = load8<T, kWide, kShared>(in.h, k, sp);
+      o[k] = load8<T, kA, kShared>(in.h, k, sp);
       if (f.has_post) {
-        y[k] = load8<T, kWide, kShared>(in.y, k, sp) * ry;
-        const V8 z = y[k] * load8<W, kWide, kShared>(wt.post, k, sp);
-        o[k] = fma8(gated<T, W, kWide, kShared>(f, z, sg, in, wt, k, sp), 1.f, o[k]);
+        y[k] = load8<T, kA, kShared>(in.y, k, sp) * ry;
+        const V8 z = y[k] * weight8<W, kA, kShared>(wt.post, k, sp);
+        o[k] = fma8(gated<T, W, kA, kShared>(f, z, sg, in, wt, k, sp), 1.f, o[k]);
       }
       o[k] = o[k] * ro;
-      e[k] = load8<T, kWide, kShared>(in.d_next, k, sp);
+      e[k] = load8<T, kA, kShared>(in.d_next, k, sp);
       s.pre[k] = fma8(e[k], o[k], s.pre[k]);
-      e[k] = e[k] * load8<W, kWide, kShared>(wt.pre, k, sp);
+      e[k] = e[k] * weight8<W, kA, kShared>(wt.pre, k, sp);
       dot8(e[k], o[k], q);
     }
     const float m = sum(q.x + q.y) * inv;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      d[k] = a.d_out ? load8<T, kWide, kShared>(in.d_out, k, sp) : all8(0.f);
+      d[k] = a.d_out ? load8<T, kA, kShared>(in.d_out, k, sp) : all8(0.f);
       d[k] = fma8(e[k], ro, fma8(o[k], -ro * m, d[k]));
     }
   } else {
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      y[k] = load8<T, kWide, kShared>(in.y, k, sp) * ry;
-      d[k] = a.d_out ? load8<T, kWide, kShared>(in.d_out, k, sp) : all8(0.f);
+      y[k] = load8<T, kA, kShared>(in.y, k, sp) * ry;
+      d[k] = a.d_out ? load8<T, kA, kShared>(in.d_out, k, sp) : all8(0.f);
     }
   }
 #pragma unroll
-  for (int k = 0; k < kV; ++k) store8<T, kWide>(static_cast<T*>(a.d_h) + row * a.ld_d_h, k, sp, d[k]);
+  for (int k = 0; k < kV; ++k) store8<T, kA>(static_cast<T*>(a.d_h) + row * a.ld_d_h, k, sp, d[k]);
   if (f.has_post) {
     const bool token = f.gate_kind == kGateToken, full = f.gate_kind == kGateFull;
     float2 q = both(0.f), qg = both(0.f);   // b . ny, and a token's gate gradient
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      const V8 w = load8<W, kWide, kShared>(wt.post, k, sp);
-      const V8 dz = gated<T, W, kWide, kShared>(f, d[k], sg, in, wt, k, sp);
+      const V8 w = weight8<W, kA, kShared>(wt.post, k, sp);
+      const V8 dz = gated<T, W, kA, kShared>(f, d[k], sg, in, wt, k, sp);
       if (token) dot8(d[k], y[k] * w, qg);
       if (full)
-        store8<T, kWide>(static_cast<T*>(a.d_gate) + row * a.ld_d_gate, k, sp, d[k] * (y[k] * w) * f.scale);
+        store8<T, kA>(static_cast<T*>(a.d_gate) + row * a.ld_d_gate, k, sp, d[k] * (y[k] * w) * f.scale);
       s.post[k] = fma8(token || full ? dz : d[k] * f.scale, y[k], s.post[k]);
       d[k] = dz * w;
       dot8(d[k], y[k], q);
@@ -369,16 +443,17 @@ __device__ __forceinline__ void row_backward(const NormGradArgs& a, int64_t row,
     m *= inv;
 #pragma unroll
     for (int k = 0; k < kV; ++k)
-      store8<T, kWide>(static_cast<T*>(a.d_y) + row * a.ld_d_y, k, sp, fma8(d[k], ry, y[k] * (-ry * m)));
+      store8<T, kA>(static_cast<T*>(a.d_y) + row * a.ld_d_y, k, sp, fma8(d[k], ry, y[k] * (-ry * m)));
   } else {
     read();
   }
 }
 
 // The CTA's partial row: [which][cols to 8], which = d_post, d_pre, d_gate (as wanted).
-template <typename W, int kV, bool kWide, bool kShared>
+template <typename W, int kV, Access kA, bool kShared>
 __device__ __forceinline__ void store_sums(const NormGradArgs& a, const Weights<W>& wt, const ColumnSums<kV>& s,
                                            int threads) {
+  constexpr Access kSumAccess = kA == kStrided ? kStrided : kAligned;   // the partial rows are padded to whole vectors
   const Span sp = {a.f.cols, threads};
   const int64_t padded = (sp.cols + 7) / 8 * 8;
   float* p = a.partial + (int64_t)blockIdx.x * a.n_sums * padded;
@@ -388,13 +463,13 @@ __device__ __forceinline__ void store_sums(const NormGradArgs& a, const Weights<
     if (a.f.has_post) {
       V8 post = s.post[k];
       if (a.f.gate_kind == kGateFeature) {
-        store8<float, kWide>(q + (a.f.pre ? 2 : 1) * padded, k, sp, post * load8<W, kWide, kShared>(wt.post, k, sp));
-        post = post * load8<W, kWide, kShared>(wt.gate, k, sp);
+        store8<float, kSumAccess>(q + (a.f.pre ? 2 : 1) * padded, k, sp, post * weight8<W, kA, kShared>(wt.post, k, sp));
+        post = post * weight8<W, kA, kShared>(wt.gate, k, sp);
       }
-      store8<float, kWide>(q, k, sp, post);
+      store8<float, kSumAccess>(q, k, sp, post);
       q += padded;
     }
-    if (a.f.pre) store8<float, kWide>(q, k, sp, s.pre[k]);
+    if (a.f.pre) store8<float, kSumAccess>(q, k, sp, s.pre[k]);
   }
 }
 
@@ -419,16 +494,16 @@ __device__ __forceinline__ Row<T> global_row(const NormArgs& a, int64_t row) {
 }
 
 // One CTA per row, everything from global memory.
-template <typename T, typename W, int kV, bool kWide>
+template <typename T, typename W, int kV, Access kA>
 __global__ void __launch_bounds__(kV == 1 ? 1024 : 512) norm_kernel(const NormArgs a) {
   __shared__ float2 s_sum[64];
   BlockSum sum{s_sum, (int)blockDim.x};
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x)
-    row_forward<T, W, kV, kWide, false>(a, row, global_row<T>(a, row), global_weights<T, W>(a), sum, [] {});
+    row_forward<T, W, kV, kA, false>(a, row, global_row<T>(a, row), global_weights<T, W>(a), sum, [] {});
 }
-template <typename T, typename W, int kV, bool kWide>
+template <typename T, typename W, int kV, Access kA>
 __global__ void __launch_bounds__(512) norm_grad_kernel(const NormGradArgs a) {
   __shared__ float2 s_sum[64];
   BlockSum sum{s_sum, (int)blockDim.x};
@@ -440,9 +515,9 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(const NormGradArgs a) {
     Row<T> in = global_row<T>(a.f, row);
     in.d_out = static_cast<const T*>(a.d_out) + row * a.ld_d_out;
     in.d_next = static_cast<const T*>(a.d_next) + row * a.ld_d_next;
-    row_backward<T, W, kV, kWide, false>(a, row, stats_of(a.f, row), in, global_weights<T, W>(a.f), sum, s, [] {});
+    row_backward<T, W, kV, kA, false>(a, row, stats_of(a.f, row), in, global_weights<T, W>(a.f), sum, s, [] {});
   }
-  store_sums<W, kV, kWide, false>(a, global_weights<T, W>(a.f), s, blockDim.x);
+  store_sums<W, kV, kA, false>(a, global_weights<T, W>(a.f), s, blockDim.x);
 }
 
 // ---- persistent CTAs over a ring of rows -------------------------------------
@@ -461,7 +536,7 @@ struct Ring {
 // granule lies in one page, so that its bytes beside the row can be read, and
 // they are not used).  The last warp issues the copies: in a computing thread
 // they would hold up every barrier of the row (2.1 us a row against 1.3).
-template <typename T, typename W, int kV, bool kWide, bool kGrad>
+template <typename T, typename W, int kV, Access kA, bool kGrad>
 __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormGradArgs a, const Ring ring) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 s_sum[64];
@@ -525,7 +600,8 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
   }
   // -------------------------------------------------------------- rows
   BlockSum sum{s_sum, threads};
-  // this thread's columns of the weights, for this thread alone
+  // this thread's columns of the weights, for this thread alone, whole vectors of them
+  const int padded = (f.cols + kVec - 1) / kVec * kVec;
   const int post_gate = f.has_post ? 1 + (f.gate_kind == kGateFeature ? 1 : 0) : 0;
   const Weights<W> wt = {s_w, s_w + ring.weight / sizeof(W), s_w + post_gate * (ring.weight / sizeof(W))};
   {
@@ -534,11 +610,12 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
     for (int k = 0; k < kV; ++k)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const int c = column<kWide>(threads, k, i);
-        if (c >= f.cols) continue;
-        if (f.has_post) const_cast<W*>(wt.post)[c] = g.post[c];
-        if (f.has_post && f.gate_kind == kGateFeature) const_cast<W*>(wt.gate)[c] = g.gate[c];
-        if (f.pre) const_cast<W*>(wt.pre)[c] = g.pre[c];
+        const int c = column<kA>(threads, k, i);
+        if (c >= padded) continue;
+        const bool in = c < f.cols;
+        if (f.has_post) const_cast<W*>(wt.post)[c] = in ? g.post[c] : down<W>(0.f);
+        if (f.has_post && f.gate_kind == kGateFeature) const_cast<W*>(wt.gate)[c] = in ? g.gate[c] : down<W>(0.f);
+        if (f.pre) const_cast<W*>(wt.pre)[c] = in ? g.pre[c] : down<W>(0.f);
       }
   }
   ColumnSums<kV> sums;
@@ -565,15 +642,15 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
       if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&s_empty[s]);
     };
     if (kGrad)
-      row_backward<T, W, kV, kWide, true>(a, row, now, in, wt, sum, sums, read);
+      row_backward<T, W, kV, kA, true>(a, row, now, in, wt, sum, sums, read);
     else
-      row_forward<T, W, kV, kWide, true>(f, row, in, wt, sum, read);
+      row_forward<T, W, kV, kA, true>(f, row, in, wt, sum, read);
     if (++s == ring.stages) {
       s = 0;
       ph ^= 1;
     }
   }
-  if (kGrad) store_sums<W, kV, kWide, true>(a, wt, sums, threads);
+  if (kGrad) store_sums<W, kV, kA, true>(a, wt, sums, threads);
 }
 
 // The partial rows added: lane l of a warp a column, the warps' shares of the
@@ -615,7 +692,7 @@ bool ring_shape(const NormArgs& a, bool grad, bool d_out, int v, Ring* ring) {
   const int size = type_bytes(a.type), wsize = type_bytes(a.weight_type);
   const int threads = threads_for(a.cols, v) + 32;
   if (threads > (grad ? 512 : 1024)) return false;
-  ring->slot = (a.cols * size + 16 + 127) / 128 * 128;
+  ring->slot = (a.cols * size + 64 + 127) / 128 * 128;   // up to 15 bytes before the row, and a word behind its last vector
   ring->weight = (a.cols * wsize + 127) / 128 * 128;
   ring->inputs = 1 + (a.has_post ? 1 : 0) + (a.gate_kind == kGateFull ? 1 : 0);
   if (grad) ring->inputs += (d_out ? 1 : 0) + (a.pre ? 1 : 0);
@@ -637,20 +714,23 @@ bool ring_shape(const NormArgs& a, bool grad, bool d_out, int v, Ring* ring) {
 // CTA has more warps with one (fp32 weights: 59 us against 65).
 int ring_for(const NormArgs& a, bool grad, bool d_out, Ring* ring) {
   const int vecs = vectors(a.cols);
+  const bool single = !a.wide && a.type == kF32;
   if (a.rows < 2 * sm_count()) return 0;
   if (grad) {
-    // single accesses with two vectors per thread spill (4567 columns: 414 us against 224 with one CTA per row)
-    if (a.wide && vecs > 64 && ring_shape(a, grad, d_out, 2, ring)) return 2;
-    return (a.wide ? vecs <= 64 : vecs <= 480) && ring_shape(a, grad, d_out, 1, ring) ? 1 : 0;
+    // (single accesses with two vectors per thread spill)
+    if (vecs > 64 && !single && ring_shape(a, grad, d_out, 2, ring)) return 2;
+    return (vecs <= 64 || single) && ring_shape(a, grad, d_out, 1, ring) ? 1 : 0;
   }
-  if (a.wide && vecs > 64 && ring_shape(a, grad, d_out, 2, ring) && ring->ctas >= 2) return 2;
+  if (vecs > 64 && !single && ring_shape(a, grad, d_out, 2, ring) && ring->ctas >= 2) return 2;
   if (ring_shape(a, grad, d_out, 1, ring)) return 1;
   return ring_shape(a, grad, d_out, 2, ring) ? 2 : 0;
 }
 
 template <typename T, typename W, int kV, bool kWide, bool kGrad>
 cudaError_t launch_rows(const NormGradArgs& a, const Ring& ring, cudaStream_t st) {
-  auto* kernel = rows_kernel<T, W, kV, kWide, kGrad>;
+  // rows that are not aligned: 16-bit values by shifted words (4096 x 4567 bf16, backward: 204 us against 376 by single
+  // accesses), 32-bit values by single accesses (777 x 1003: 6 us forward against 11 by shifted words)
+  auto* kernel = rows_kernel<T, W, kV, kWide ? kAligned : sizeof(T) == 2 ? kShifted : kStrided, kGrad>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring.smem());
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, dim3((unsigned)std::min(a.f.rows, ring.ctas * sm_count())),
@@ -659,6 +739,7 @@ cudaError_t launch_rows(const NormGradArgs& a, const Ring& ring, cudaStream_t st
 
 template <typename T, typename W, bool kWide>
 cudaError_t forward(const NormArgs& a, cudaStream_t st) {
+  constexpr Access kA = kWide ? kAligned : kStrided;
   Ring ring;
   const int vr = ring_for(a, false, false, &ring);
   if (vr) {
@@ -670,8 +751,8 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
   const int v = vecs <= 1024 ? 1 : 4;
   const int threads = threads_for(a.cols, v);
   const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 1 << 20);
-  if (v == 1) return launch_dependent(norm_kernel<T, W, 1, kWide>, dim3(grid), dim3(threads), 0, st, 1, a);
-  return launch_dependent(norm_kernel<T, W, 4, kWide>, dim3(grid), dim3(threads), 0, st, 1, a);
+  if (v == 1) return launch_dependent(norm_kernel<T, W, 1, kA>, dim3(grid), dim3(threads), 0, st, 1, a);
+  return launch_dependent(norm_kernel<T, W, 4, kA>, dim3(grid), dim3(threads), 0, st, 1, a);
 }
 
 // CTAs of the backward, one partial row each
@@ -682,6 +763,7 @@ int grad_parts(const NormArgs& a, int v, const Ring& ring) {
 
 template <typename T, typename W, bool kWide>
 cudaError_t backward(NormGradArgs a, cudaStream_t st) {
+  constexpr Access kA = kWide ? kAligned : kStrided;
   Ring ring;
   const int vr = ring_for(a.f, true, a.d_out != nullptr, &ring);
   a.n_parts = grad_parts(a.f, vr, ring);
@@ -690,9 +772,9 @@ cudaError_t backward(NormGradArgs a, cudaStream_t st) {
   cudaError_t e;
   if (vr == 1) e = launch_rows<T, W, 1, kWide, true>(a, ring, st);
   else if (vr == 2) e = launch_rows<T, W, 2, kWide, true>(a, ring, st);
-  else if (v == 1) e = launch_dependent(norm_grad_kernel<T, W, 1, kWide>, grid, threads, 0, st, 1, a);
-  else if (v == 2) e = launch_dependent(norm_grad_kernel<T, W, 2, kWide>, grid, threads, 0, st, 1, a);
-  else e = launch_dependent(norm_grad_kernel<T, W, 4, kWide>, grid, threads, 0, st, 1, a);
+  else if (v == 1) e = launch_dependent(norm_grad_kernel<T, W, 1, kA>, grid, threads, 0, st, 1, a);
+  else if (v == 2) e = launch_dependent(norm_grad_kernel<T, W, 2, kA>, grid, threads, 0, st, 1, a);
+  else e = launch_dependent(norm_grad_kernel<T, W, 4, kA>, grid, threads, 0, st, 1, a);
   if (e != cudaSuccess) return e;
   W* o[3];
   int n = 0;

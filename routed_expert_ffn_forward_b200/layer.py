@@ -114,6 +114,8 @@ class MoELayer:
 
     def forward_mx(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """The layer's forward over the MXFP4 products (see ``moe_forward_mx``)."""
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.H or not x.is_contiguous():
+            raise ValueError(f"x must be contiguous bfloat16 [T, {self.H}], not {x.dtype} {tuple(x.shape)}")
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device)

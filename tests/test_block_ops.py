@@ -152,6 +152,7 @@ def test_tensor_checks():
         lambda: block.mx_product(rows, weights, off, torch.zeros(4)),
         lambda: block.mx_product(rows, weights, off, out_dtype=torch.float16),
         lambda: block.mx_product(rows._replace(cols=65), weights, off),
+        lambda: block.mx_product(rows, weights._replace(rows=300), off),     # an image of other weights
         lambda: block.mx_product(rows, one, out=torch.zeros((4, 99), dtype=bf)),
         lambda: block.mx_product(rows, one, out=torch.zeros((100, 4), dtype=bf).t()),
         lambda: block.mx_product(rows, one),                                 # not on a GPU

@@ -132,6 +132,8 @@ def test_forward_mx_refusals(layer):
     assert e.value.status == moe.MOE_ERR_INVALID_ARG
     with pytest.raises(ValueError):
         L.set_mx_experts(L.mx[1], L.mx[0])
+    with pytest.raises(ValueError):
+        L.forward_mx(torch.zeros((L.H, 4), device="cuda", dtype=torch.bfloat16).t())
     from routed_expert_ffn_forward_b200.layer import MoELayer
     M = MoELayer(256, 128, 4, 2, 0)
     try:
@@ -188,3 +190,34 @@ def test_block_and_balance_loss(layer, T, mx):
     assert bool(((f(d_logits) - dw).abs() <= 4e-5 * dw.abs().max()).all())
     with pytest.raises(ValueError):
         L.forward_block(h.float(), pre)
+
+
+def test_train_step_captured_through_autograd_grad(layer):
+    """The router's and the norms' gradients through autograd, eager and in a graph."""
+    L = layer
+    T = 24
+    x = activations(T, 9)
+    L.forward(x)
+    logits, ids = L.logits(T).requires_grad_(), L.routing(T)[0]
+    h = torch.randn((T, L.H), device="cuda").bfloat16().requires_grad_()
+    w = torch.ones(L.H, device="cuda").requires_grad_()
+    y = x.float().mul(0.3).bfloat16().requires_grad_()
+
+    def step():
+        loss, _ = block.balance_loss(logits, ids, 0.01, L.gating)
+        out, nxt = block.block_norm(h, y, w, None, 0.5, w)
+        return torch.autograd.grad(loss + out.float().square().mean() + nxt.float().mean(), [logits, h, y, w])
+
+    alive = block.block_norm(h, y, w, None, 0.5, w)      # an eager graph of the same leaves
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert alive[0].shape == h.shape
