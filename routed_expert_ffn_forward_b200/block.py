@@ -12,10 +12,10 @@ Tensors that do not fit raise ValueError, refused calls of the library
 
 ``block_norm`` and ``balance_loss`` are differentiable (once); the *_forward and
 *_backward functions below them are the same operators without autograd.  A
-backward pass can be captured in a CUDA graph through those, or through
-``torch.autograd.grad``; with ``Tensor.backward`` it must not be while an eager
-graph of the same leaves is alive, as for any operator of torch (the leaves'
-gradients are then accumulated on the eager graph's stream, outside the capture).
+backward pass through autograd can be captured in a CUDA graph as long as no
+eager graph of the same leaves is alive (torch's rule for every operator: the
+leaves' nodes keep the eager graph's stream, and the capture fails); the
+*_forward and *_backward functions can always be captured.
 """
 from __future__ import annotations
 

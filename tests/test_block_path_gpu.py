@@ -192,8 +192,9 @@ def test_block_and_balance_loss(layer, T, mx):
         L.forward_block(h.float(), pre)
 
 
-def test_train_step_captured_through_autograd_grad(layer):
-    """The router's and the norms' gradients through autograd, eager and in a graph."""
+def test_train_step_captured(layer):
+    """The router's and the norms' gradients through autograd, eager and in a graph,
+    and through the functions without autograd while an eager graph is alive."""
     L = layer
     T = 24
     x = activations(T, 9)
@@ -202,13 +203,20 @@ def test_train_step_captured_through_autograd_grad(layer):
     h = torch.randn((T, L.H), device="cuda").bfloat16().requires_grad_()
     w = torch.ones(L.H, device="cuda").requires_grad_()
     y = x.float().mul(0.3).bfloat16().requires_grad_()
+    d = torch.full((T, L.H), 0.01, device="cuda", dtype=torch.bfloat16)
 
     def step():
         loss, _ = block.balance_loss(logits, ids, 0.01, L.gating)
         out, nxt = block.block_norm(h, y, w, None, 0.5, w)
-        return torch.autograd.grad(loss + out.float().square().mean() + nxt.float().mean(), [logits, h, y, w])
+        return torch.autograd.grad([loss, out, nxt], [logits, h, y, w], [torch.ones_like(loss), d, d])
 
-    alive = block.block_norm(h, y, w, None, 0.5, w)      # an eager graph of the same leaves
+    def plain():
+        with torch.no_grad():
+            loss, _, slope = block.balance_loss_forward(logits, ids, 0.01, L.gating)
+            _, _, saved = block.block_norm_forward(h, y, w, None, 0.5, w)
+            d_h, d_y, d_post, _, d_pre = block.block_norm_backward(d, d, h, y, w, None, 0.5, w, saved)
+            return block.balance_loss_backward(torch.ones_like(loss), slope, logits, L.gating), d_h, d_y, d_post + d_pre
+
     want = step()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -219,5 +227,11 @@ def test_train_step_captured_through_autograd_grad(layer):
     with torch.cuda.graph(graph):
         got = step()
     graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    alive = block.block_norm(h, y, w, None, 0.5, w)      # an eager graph of the same leaves
+    graph2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph2):
+        got = plain()
+    graph2.replay()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert alive[0].shape == h.shape
