@@ -144,19 +144,6 @@ __device__ __forceinline__ int column(int threads, int k, int i) {
 struct Span {
   int cols, threads;
 };
-// kN words of a stream of kN + 4 words from byte `shift` (0..15) on
-template <int kN>
-__device__ __forceinline__ void shifted_words(const uint32_t* w, uint32_t shift, uint32_t* out) {
-  const bool two = shift & 8, one = shift & 4;
-  const uint32_t bits = (shift & 3) * 8;
-  uint32_t t[kN + 2], u[kN + 1];
-#pragma unroll
-  for (int i = 0; i < kN + 2; ++i) t[i] = two ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < kN + 1; ++i) u[i] = one ? t[i + 1] : t[i];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) out[i] = __funnelshift_r(u[i], u[i + 1], bits);
-}
 // Vector k of a row; zeros behind its end.  Single 16-bit values are loaded
 // plainly: __ldg of a half type is an asm statement that is not volatile, so
 // the compiler may run it ahead of the test that guards it, with a pointer

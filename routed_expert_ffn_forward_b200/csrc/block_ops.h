@@ -44,6 +44,22 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+#ifdef __CUDACC__
+// kN words of a stream of kN + 4 words from byte `shift` (0..15) on
+template <int kN>
+__device__ __forceinline__ void shifted_words(const uint32_t* w, uint32_t shift, uint32_t* out) {
+  const bool two = shift & 8, one = shift & 4;
+  const uint32_t bits = (shift & 3) * 8;
+  uint32_t t[kN + 2], u[kN + 1];
+#pragma unroll
+  for (int i = 0; i < kN + 2; ++i) t[i] = two ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < kN + 1; ++i) u[i] = one ? t[i + 1] : t[i];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) out[i] = __funnelshift_r(u[i], u[i + 1], bits);
+}
+#endif
+
 // ---- MXFP4 ------------------------------------------------------------------
 // A row of `cols` values is stored as ceil(cols / 256) chunks of 256: 128 bytes
 // of E2M1 codes and 8 E8M0 scales per chunk, the padding zero codes.

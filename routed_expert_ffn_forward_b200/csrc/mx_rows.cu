@@ -26,8 +26,12 @@ __device__ __forceinline__ float to_float<__half>(__half v) { return __half2floa
 template <>
 __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Eight values to eight codes (value i in nibble i): round to nearest even, saturating.
-__device__ __forceinline__ uint32_t e2m1_codes(const float* v) {
+// Eight values times `mul` to eight codes (value i in nibble i): round to nearest even, saturating.
+__device__ __forceinline__ uint32_t e2m1_codes(const float2* v, float mul) {
+  const float2 m = make_float2(mul, mul);
+  float2 t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = __fmul2_rn(v[i], m);
   uint32_t w;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -36,102 +40,174 @@ __device__ __forceinline__ uint32_t e2m1_codes(const float* v) {
       "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(w)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+      : "f"(t[0].x), "f"(t[0].y), "f"(t[1].x), "f"(t[1].y), "f"(t[2].x), "f"(t[2].y), "f"(t[3].x), "f"(t[3].y));
   return w;
 }
-// E2M1 magnitude of a 3-bit code: codes 2..7 are floats with a one-bit
-// mantissa, 0 and 1 are 0 and 0.5.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t m = c & 7u;
-  const float a = m < 2 ? 0.5f * (float)m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
-  return c & 8u ? -a : a;
+// Two codes (a byte, the first in its low nibble) to their values in bf16, times
+// 2^(s - 127), exactly: an E2M1 value is a bf16 number with a one-bit mantissa.
+__device__ __forceinline__ uint32_t e2m1_bf16x2(uint32_t codes, float up) {
+  auto value = [&](uint32_t c) {
+    // codes 2..7 are floats 2^(c / 2 - 1) (1 + c % 2 / 2), 0 and 1 are 0 and 0.5
+    const uint32_t m = c & 7u;
+    const float a = m < 2 ? 0.5f * (float)m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
+    return __uint_as_float(__float_as_uint(a) | (c & 8u) << 28) * up;
+  };
+  const __nv_bfloat162 h = __floats2bfloat162_rn(value(codes), value(codes >> 4));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-// four nibbles (low half word) to the low nibbles of four bytes
-__device__ __forceinline__ uint32_t spread_nibbles(uint32_t v) {
-  v = (v | (v << 8)) & 0x00FF00FFu;
-  return (v | (v << 4)) & 0x0F0F0F0Fu;
+// eight nibbles to the low nibbles of eight bytes
+__device__ __forceinline__ uint2 spread_nibbles(uint32_t v) {
+  uint32_t lo = v & 0xFFFFu, hi = v >> 16;
+  lo = (lo | (lo << 8)) & 0x00FF00FFu;
+  hi = (hi | (hi << 8)) & 0x00FF00FFu;
+  return make_uint2((lo | (lo << 4)) & 0x0F0F0F0Fu, (hi | (hi << 4)) & 0x0F0F0F0Fu);
 }
 
-// Eight consecutive values of a row from column c; zeros behind its end.
+// Sixteen consecutive values of a row from column c as pairs, zeros behind its
+// end; the raw words are kept until then, so that several loads are in flight.
+// Rows that are not aligned are read in the 16-byte words that hold a byte of
+// the values (such a word lies in one page with that byte), and shifted.
 template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* __restrict__ p, int c, int cols, float* v) {
-  if (kVec && c + 8 <= cols) {
-    constexpr int kWords = sizeof(T) / 2;
-    uint4 raw[kWords];
+struct Values16 {
+  static constexpr int kWords = sizeof(T) * 16 / 16;
+  uint4 raw[kWords + (kVec ? 0 : 1)];
+  uint32_t shift;
+  __device__ __forceinline__ void load(const T* __restrict__ row, int c, int cols) {
+    const T* p = row + c;
+    shift = 0;
+    if (c + 16 <= cols) {
+      if (!kVec) shift = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+      const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) - shift);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(p + c) + i);
-    const T* e = reinterpret_cast<const T*>(raw);
+      for (int i = 0; i < kWords; ++i) raw[i] = __ldg(q + i);
+      if (!kVec && shift) raw[kWords] = __ldg(q + kWords);
+    } else {
+      T* e = reinterpret_cast<T*>(raw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float<T>(e[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_float<T>(p[c + i]) : 0.f;
+      for (int i = 0; i < 16; ++i) e[i] = c + i < cols ? p[i] : T(0.f);
+    }
   }
-}
+  __device__ __forceinline__ void pairs(float2* v) const {
+    uint32_t w[4 * kWords];
+    if (kVec) {
+#pragma unroll
+      for (int i = 0; i < 4 * kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(raw)[i];
+    } else {
+      shifted_words<4 * kWords>(reinterpret_cast<const uint32_t*>(raw), shift, w);
+    }
+    const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = make_float2(to_float<T>(e[2 * i]), to_float<T>(e[2 * i + 1]));
+  }
+};
 
-// A warp takes kU chunks of 256 columns at a time, all their loads first; eight
-// consecutive values per lane, so that a run is a quad of lanes and its
-// maximum two shuffles.  Bound by HBM (7168 x 2048 fp32: see kU in quantize).
+// A half warp takes kU chunks of 256 columns at a time, all their loads first;
+// sixteen consecutive values per lane, so that a run is a pair of lanes, its
+// maximum one shuffle and its bytes one trade of a word: lane 0 writes bytes
+// 0..7 (elements 0..7 with 16..23), lane 1 bytes 8..15.  Bound by instruction
+// issue for 16-bit values (with eight values per lane and a division per chunk
+// 4096 x 7168 bf16 took 22.7 us), by HBM for 32-bit ones.
 template <typename T, bool kVec, int kU>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, int64_t ld, uint32_t n, int cols, uint32_t kc,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                                                        __nv_bfloat16* __restrict__ values) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const uint32_t step = gridDim.x * (blockDim.x >> 5) * kU;
-  for (uint32_t w0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kU; w0 < n; w0 += step) {
-    float v[kU][8];
+  __shared__ uint4 s_values[kVec ? 1 : 256 * 2];   // a lane's 16 values, where rows of values are not aligned
+  const uint32_t lane = threadIdx.x & 15;
+  const uint32_t halves = gridDim.x * (blockDim.x >> 4), step = halves * kU;
+  uint32_t w0 = (blockIdx.x * (blockDim.x >> 4) + (threadIdx.x >> 4)) * kU;
+  // (row, chunk) of w0, kept without a division per chunk
+  uint32_t row0 = w0 / kc, chunk0 = w0 - row0 * kc;
+  const uint32_t step_rows = step / kc, step_chunks = step - step_rows * kc;
+  // a warp stays whole: its upper half may be behind the end
+  for (uint32_t first = w0 - (threadIdx.x >> 4 & 1) * kU; first < n; first += step, w0 += step) {
+    Values16<T, kVec> in[kU];
+    uint32_t row = row0, chunk = chunk0;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const uint32_t w = min(w0 + u, n - 1), row = w / kc;
-      load8<T, kVec>(x + row * ld, (w - row * kc) * kMxChunk + lane * 8, cols, v[u]);
+      in[u].load(x + row * ld, w0 + u < n ? (int)(chunk * kMxChunk + lane * 16) : cols, cols);
+      if (++chunk == kc) {
+        chunk = 0;
+        row = min(row + 1, (n - 1) / kc);
+      }
     }
+    row = row0;
+    chunk = chunk0;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const uint32_t w = w0 + u;
-      if (w >= n) break;
+      float2 v[8];
+      in[u].pairs(v);
       uint32_t top = 0;   // magnitude bits order like the magnitudes, NaN above all
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[u][i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < 8; ++i)
+        top = max(top, max(__float_as_uint(v[i].x) & 0x7FFFFFFFu, __float_as_uint(v[i].y) & 0x7FFFFFFFu));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int ef = (int)(top >> 23);
       const int s = ef == 255 ? 255 : max(ef - 2, 0);
       const float mul = __uint_as_float((uint32_t)(254 - min(s, 253)) << 23);   // 2^(127 - s)
-      float t[8];
+      const uint32_t a = e2m1_codes(v, mul), b = e2m1_codes(v + 4, mul);   // this lane's first and last eight
+      const bool upper = lane & 1;   // elements 16..31 of the run
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 1);
+      const uint2 lo = spread_nibbles(upper ? other : a), hi = spread_nibbles(upper ? b : other);
+      if (w < n) {
+        reinterpret_cast<uint2*>(codes)[(size_t)w * 16 + lane] = make_uint2(lo.x | hi.x << 4, lo.y | hi.y << 4);
+        if (!upper) scales[(size_t)w * 8 + (lane >> 1)] = (uint8_t)s;
+        if (values) {
+          // 2^(s - 127); s = 0 is the subnormal 2^-127, s = 255 stands for NaN
+          const float up = s == 255 ? __uint_as_float(0x7FC00000u) : s ? __uint_as_float((uint32_t)s << 23)
+                                                                       : __uint_as_float(0x00400000u);
+          const int c0 = (int)(chunk * kMxChunk + lane * 16);
+          __nv_bfloat16* q = values + (size_t)row * cols + c0;
+          uint32_t o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = v[u][i] * mul;
-      const uint32_t w8 = e2m1_codes(t);
-      // lanes q and q ^ 2 of a quad hold elements j.. and 16 + j..: each writes
-      // one 32-bit word that pairs four of the lower with four of the upper
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, w8, 2);
-      const bool upper = lane & 2;
-      const uint32_t lo = upper ? other >> 16 : w8 & 0xFFFFu;
-      const uint32_t hi = upper ? w8 >> 16 : other & 0xFFFFu;
-      const int word = (lane & ~3) + 2 * (lane & 1) + (upper ? 1 : 0);
-      reinterpret_cast<uint32_t*>(codes)[(size_t)w * 32 + word] = spread_nibbles(lo) | spread_nibbles(hi) << 4;
-      if ((lane & 3) == 0) scales[(size_t)w * 8 + (lane >> 2)] = (uint8_t)s;
-      if (values) {
-        // 2^(s - 127); s = 0 is the subnormal 2^-127, s = 255 stands for NaN
-        const float up = s == 255 ? __uint_as_float(0x7FC00000u) : s ? __uint_as_float((uint32_t)s << 23)
-                                                                     : __uint_as_float(0x00400000u);
-        __nv_bfloat162 o[4];
+          for (int i = 0; i < 4; ++i) {
+            o[i] = e2m1_bf16x2(a >> (8 * i), up);
+            o[4 + i] = e2m1_bf16x2(b >> (8 * i), up);
+          }
+          if (kVec) {
+            if (c0 + 16 <= cols) {
+              reinterpret_cast<uint4*>(q)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+              reinterpret_cast<uint4*>(q)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            } else {
+              const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)   // exact
-          o[i] = __floats2bfloat162_rn(e2m1_value(w8 >> (8 * i)) * up, e2m1_value(w8 >> (8 * i + 4)) * up);
-        const uint32_t row = w / kc;
-        const int c0 = (w - row * kc) * kMxChunk + lane * 8;
-        __nv_bfloat16* q = values + (size_t)row * cols + c0;
-        if (kVec && c0 + 8 <= cols && cols % 8 == 0) {
-          *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c0 + i < cols) q[i] = i & 1 ? o[i >> 1].y : o[i >> 1].x;
+              for (int i = 0; i < 16; ++i)
+                if (c0 + i < cols) q[i] = e[i];
+            }
+          } else {
+            uint4* mine = s_values + threadIdx.x * 2;
+            mine[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            mine[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
         }
       }
+      if (!kVec && values) {
+        // neighbouring lanes store neighbouring values of the half warp's chunk
+        __syncwarp();
+        if (w < n) {
+          const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(s_values + (threadIdx.x & ~15) * 2);
+          const int c0 = (int)(chunk * kMxChunk + lane);
+          __nv_bfloat16* q = values + (size_t)row * cols + c0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c0 + 16 * i < cols) q[16 * i] = e[lane + 16 * i];
+        }
+        __syncwarp();
+      }
+      if (++chunk == kc) {
+        chunk = 0;
+        ++row;
+      }
     }
+    row0 += step_rows;
+    chunk0 += step_chunks;
+    if (chunk0 >= kc) {
+      chunk0 -= kc;
+      ++row0;
+    }
+    row0 = min(row0, (n - 1) / kc);   // the upper half of the last warp loads nothing, from a row that is there
   }
 }
 
@@ -172,10 +248,10 @@ template <typename T, bool kVec>
 cudaError_t quantize_as(const T* x, int64_t ld, uint32_t n, int cols, uint8_t* codes, uint8_t* scales,
                         __nv_bfloat16* values, cudaStream_t st) {
   const uint32_t kc = mx_chunks(cols), sms = sm_count();
-  // a chunk per warp until the GPU is full of warps, then four
-  const bool many = n > sms * 64;
-  const unsigned blocks = std::min(many ? (n + 31) / 32 : (n + 7) / 8, sms * 8);
-  auto* kernel = many ? quantize_kernel<T, kVec, 4> : quantize_kernel<T, kVec, 1>;
+  // a chunk per half warp until the GPU is full of them, then two
+  const bool many = n > sms * 128;
+  const unsigned blocks = std::min(many ? (n + 31) / 32 : (n + 15) / 16, sms * 8);
+  auto* kernel = many ? quantize_kernel<T, kVec, 2> : quantize_kernel<T, kVec, 1>;
   return launch_dependent(kernel, dim3(blocks), dim3(256), 0, st, 1, x, ld, n, cols, kc, codes, scales, values);
 }
 template <typename T>
@@ -184,7 +260,7 @@ cudaError_t quantize(const void* p, int64_t ld, int rows, int cols, uint8_t* cod
   const T* x = static_cast<const T*>(p);
   const uint32_t n = (uint32_t)rows * mx_chunks(cols);
   const bool vec = (reinterpret_cast<uintptr_t>(x) % 16 == 0) && (ld * sizeof(T)) % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(values) % 16 == 0;
+                   (!values || (reinterpret_cast<uintptr_t>(values) % 16 == 0 && cols % 8 == 0));
   return vec ? quantize_as<T, true>(x, ld, n, cols, codes, scales, values, st)
              : quantize_as<T, false>(x, ld, n, cols, codes, scales, values, st);
 }
