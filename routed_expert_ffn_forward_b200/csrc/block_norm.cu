@@ -137,12 +137,12 @@ enum Access { kStrided, kAligned, kShifted };
 // The eight columns of vector k of this thread: consecutive ones, or with
 // kStrided every threads-th, so that a warp's single accesses stay side by side.
 template <Access kA>
-__device__ __forceinline__ int column(int threads, int k, int i) {
-  return kA != kStrided ? (threadIdx.x + k * threads) * kVec + i : threadIdx.x + (k * kVec + i) * threads;
+__device__ __forceinline__ int column(int tid, int threads, int k, int i) {
+  return kA != kStrided ? (tid + k * threads) * kVec + i : tid + (k * kVec + i) * threads;
 }
-// A row's columns and the threads that share them.
+// A row's columns, the threads that share them and this one's number among them.
 struct Span {
-  int cols, threads;
+  int cols, threads, tid;
 };
 // Vector k of a row; zeros behind its end.  Single 16-bit values are loaded
 // plainly: __ldg of a half type is an asm statement that is not volatile, so
@@ -155,12 +155,12 @@ __device__ __forceinline__ V8 load8(const T* row, int k, const Span& sp) {
   if (kA == kStrided) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int c = column<kStrided>(sp.threads, k, i);
+      const int c = column<kStrided>(sp.tid, sp.threads, k, i);
       if (c < sp.cols) v.set(i, up(row[c]));
     }
     return v;
   }
-  const int c = column<kAligned>(sp.threads, k, 0);
+  const int c = column<kAligned>(sp.tid, sp.threads, k, 0);
   if (c >= sp.cols) return v;
   if (kA == kAligned) {
     uint4 raw[kWords];
@@ -190,12 +190,12 @@ __device__ __forceinline__ void store8(T* row, int k, const Span& sp, const V8& 
   if (kA == kStrided) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int c = column<kStrided>(sp.threads, k, i);
+      const int c = column<kStrided>(sp.tid, sp.threads, k, i);
       if (c < sp.cols) row[c] = down<T>(v.get(i));
     }
     return;
   }
-  const int c = column<kAligned>(sp.threads, k, 0);
+  const int c = column<kAligned>(sp.tid, sp.threads, k, 0);
   if (kA == kAligned) {
     if (c >= sp.cols) return;
     uint4 raw[kWords];
@@ -238,13 +238,13 @@ __device__ __forceinline__ void store8(T* row, int k, const Span& sp, const V8& 
   }
 }
 
-// Sums over a CTA's threads, the same in every one; the order depends on the CTA's
-// size alone.  `s` holds 2 x 32 pairs, used in turn.
+// Sums over a team's threads, the same in every one; the order depends on the
+// team's size alone.  `s` holds 2 x 32 pairs, used in turn.
 struct BlockSum {
   float2* s;
-  int threads;   // the CTA's first so many
+  int threads, tid, barrier;   // a team of the CTA: its size, this thread's number in it, its barrier
   int turn = 0;
-  __device__ __forceinline__ void sync() const { ptx::named_barrier_sync(1, threads); }
+  __device__ __forceinline__ void sync() const { ptx::named_barrier_sync(barrier, threads); }
   __device__ __forceinline__ float2 operator()(float2 v) {
     const int warps = threads >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -255,7 +255,7 @@ struct BlockSum {
     if (warps == 1) return v;
     float2* b = s + 32 * turn;
     turn ^= 1;   // the previous sum may still be read
-    if (lane == 0) b[threadIdx.x >> 5] = v;
+    if (lane == 0) b[tid >> 5] = v;
     sync();
     v = lane < warps ? b[lane] : make_float2(0.f, 0.f);
 #pragma unroll
@@ -272,7 +272,7 @@ struct BlockSum {
     if (warps == 1) return v;
     float* b = reinterpret_cast<float*>(s + 32 * turn);
     turn ^= 1;
-    if (lane == 0) b[threadIdx.x >> 5] = v;
+    if (lane == 0) b[tid >> 5] = v;
     sync();
     v = lane < warps ? b[lane] : 0.f;
 #pragma unroll
@@ -318,7 +318,7 @@ template <typename T, typename W, int kV, Access kA, bool kShared, typename Read
 __device__ __forceinline__ void row_forward(const NormArgs& a, int64_t row, const Row<T>& in, const Weights<W>& wt,
                                             BlockSum& sum, Read read) {
   const float inv = 1.f / (float)a.cols;
-  const Span sp = {a.cols, sum.threads};
+  const Span sp = {a.cols, sum.threads, sum.tid};
   V8 o[kV];
   if (a.has_post) {
     V8 y[kV];
@@ -330,7 +330,7 @@ __device__ __forceinline__ void row_forward(const NormArgs& a, int64_t row, cons
     }
     const float sg = token_scale(a, in);
     const float r = rsqrtf(sum(q.x + q.y) * inv + a.eps);
-    if (threadIdx.x == 0 && a.stats) a.stats[2 * row] = r;
+    if (sp.tid == 0 && a.stats) a.stats[2 * row] = r;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       const V8 z = y[k] * weight8<W, kA, kShared>(wt.post, k, sp);
@@ -347,7 +347,7 @@ __device__ __forceinline__ void row_forward(const NormArgs& a, int64_t row, cons
 #pragma unroll
     for (int k = 0; k < kV; ++k) dot8(o[k], o[k], q);
     const float r = rsqrtf(sum(q.x + q.y) * inv + a.eps);
-    if (threadIdx.x == 0 && a.stats) a.stats[2 * row + 1] = r;
+    if (sp.tid == 0 && a.stats) a.stats[2 * row + 1] = r;
 #pragma unroll
     for (int k = 0; k < kV; ++k)
       store8<T, kA>(static_cast<T*>(a.next) + row * a.ld_next, k, sp,
@@ -369,7 +369,7 @@ __device__ __forceinline__ void row_backward(const NormGradArgs& a, int64_t row,
                                              const Weights<W>& wt, BlockSum& sum, ColumnSums<kV>& s, Read read) {
   const NormArgs& f = a.f;
   const float inv = 1.f / (float)f.cols, ry = stats.x, ro = stats.y;
-  const Span sp = {f.cols, sum.threads};
+  const Span sp = {f.cols, sum.threads, sum.tid};
   const float sg = f.has_post ? token_scale(f, in) : 0.f;
   V8 y[kV], d[kV];   // y: y / rms(y); d: the gradient of out
   if (f.pre) {
@@ -423,7 +423,7 @@ __device__ __forceinline__ void row_backward(const NormGradArgs& a, int64_t row,
     if (token) {
       const float2 t = sum(make_float2(q.x + q.y, qg.x + qg.y));
       m = t.x;
-      if (threadIdx.x == 0) static_cast<T*>(a.d_gate)[row * a.ld_d_gate] = down<T>(t.y * f.scale);
+      if (sp.tid == 0) static_cast<T*>(a.d_gate)[row * a.ld_d_gate] = down<T>(t.y * f.scale);
     } else {
       m = sum(q.x + q.y);
     }
@@ -441,7 +441,7 @@ template <typename W, int kV, Access kA, bool kShared>
 __device__ __forceinline__ void store_sums(const NormGradArgs& a, const Weights<W>& wt, const ColumnSums<kV>& s,
                                            int threads) {
   constexpr Access kSumAccess = kA == kStrided ? kStrided : kAligned;   // the partial rows are padded to whole vectors
-  const Span sp = {a.f.cols, threads};
+  const Span sp = {a.f.cols, threads, (int)threadIdx.x};
   const int64_t padded = (sp.cols + 7) / 8 * 8;
   float* p = a.partial + (int64_t)blockIdx.x * a.n_sums * padded;
 #pragma unroll
@@ -484,7 +484,7 @@ __device__ __forceinline__ Row<T> global_row(const NormArgs& a, int64_t row) {
 template <typename T, typename W, int kV, Access kA>
 __global__ void __launch_bounds__(kV == 1 ? 1024 : 512) norm_kernel(const NormArgs a) {
   __shared__ float2 s_sum[64];
-  BlockSum sum{s_sum, (int)blockDim.x};
+  BlockSum sum{s_sum, (int)blockDim.x, (int)threadIdx.x, 1};
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x)
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kV == 1 ? 1024 : 512) norm_kernel(const NormAr
 template <typename T, typename W, int kV, Access kA>
 __global__ void __launch_bounds__(512) norm_grad_kernel(const NormGradArgs a) {
   __shared__ float2 s_sum[64];
-  BlockSum sum{s_sum, (int)blockDim.x};
+  BlockSum sum{s_sum, (int)blockDim.x, (int)threadIdx.x, 1};
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   ColumnSums<kV> s;
@@ -512,7 +512,8 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(const NormGradArgs a) {
 __device__ unsigned g_norm_err = 0;
 
 struct Ring {
-  int stages, inputs, slot;   // stages of so many input rows of `slot` bytes
+  int teams;                  // of threads in a CTA, each with rows and stages of its own
+  int stages, inputs, slot;   // stages (of all teams) of so many input rows of `slot` bytes
   int weights, weight;        // weight vectors and the bytes of one
   int ctas;                   // per SM
   size_t smem() const { return (size_t)weights * weight + (size_t)stages * inputs * slot; }
@@ -523,13 +524,13 @@ struct Ring {
 // granule lies in one page, so that its bytes beside the row can be read, and
 // they are not used).  The last warp issues the copies: in a computing thread
 // they would hold up every barrier of the row (2.1 us a row against 1.3).
-template <typename T, typename W, int kV, Access kA, bool kGrad>
+template <typename T, typename W, int kV, Access kA, bool kGrad, int kTeams>
 __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormGradArgs a, const Ring ring) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 s_sum[64];
+  __shared__ float2 s_sum[2][64];
   __shared__ uint64_t s_full[8], s_empty[8];
   const NormArgs& f = a.f;
-  const int threads = blockDim.x - 32;
+  const int threads = (blockDim.x - 32) / kTeams, stages = ring.stages / kTeams;
   W* s_w = reinterpret_cast<W*>(smem);
   uint8_t* s_rows = smem + ring.weights * ring.weight;
   const T* src[5] = {static_cast<const T*>(f.h), static_cast<const T*>(f.y),
@@ -550,17 +551,23 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   __syncthreads();
+  // the last warp's lanes copy for one team each
+  const bool copies = threadIdx.x >= threads * kTeams;
+  const int lane = threadIdx.x & 31, team = kTeams == 1 ? 0 : copies ? lane & (kTeams - 1) : threadIdx.x / threads;
+  const int64_t first = (int64_t)blockIdx.x * kTeams + team, step = (int64_t)gridDim.x * kTeams;
+  uint64_t *full = s_full + team * stages, *empty = s_empty + team * stages;
+  s_rows += (size_t)team * stages * ring.inputs * ring.slot;
   int s = 0;
   uint32_t ph = 0;
-  if (threadIdx.x >= threads) {
+  if (copies) {
     // ------------------------------------------------------------ copies
-    if (threadIdx.x > threads) return;
+    if (lane >= kTeams) return;   // lane l copies for team l
     const uint32_t bytes = f.cols * sizeof(T);
     ptx::IssueLog log;
-    for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x) {
-      if (!ptx::mbar_wait(&s_empty[s], ph ^ 1u)) {
+    for (int64_t row = first; row < f.rows; row += step) {
+      if (!ptx::mbar_wait(&empty[s], ph ^ 1u)) {
         atomicOr(&g_norm_err, 1u);
-        log.drain(s_full, ring.stages);   // never leave with a copy into shared memory in flight
+        log.drain(full, stages);   // never leave with a copy into shared memory in flight
         return;
       }
       uintptr_t p[5];
@@ -571,14 +578,14 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
         n[i] = src[i] ? ((uint32_t)(p[i] & 15) + bytes + 15) & ~15u : 0;
         total += n[i];
       }
-      ptx::mbar_arrive_expect_tx(&s_full[s], total);
+      ptx::mbar_arrive_expect_tx(&full[s], total);
 #pragma unroll
       for (int i = 0; i < 5; ++i)
         if (n[i])
           ptx::bulk_load(s_rows + ((size_t)s * ring.inputs + place[i]) * ring.slot,
-                         reinterpret_cast<const void*>(p[i] & ~(uintptr_t)15), n[i], &s_full[s]);
+                         reinterpret_cast<const void*>(p[i] & ~(uintptr_t)15), n[i], &full[s]);
       log.note(s, ph);
-      if (++s == ring.stages) {
+      if (++s == stages) {
         s = 0;
         ph ^= 1;
       }
@@ -586,8 +593,9 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
     return;
   }
   // -------------------------------------------------------------- rows
-  BlockSum sum{s_sum, threads};
-  // this thread's columns of the weights, for this thread alone, whole vectors of them
+  const int tid = threadIdx.x - team * threads;
+  BlockSum sum{s_sum[team], threads, tid, 1 + team};
+  // this thread's columns of the weights, whole vectors of them (every team writes the same)
   const int padded = (f.cols + kVec - 1) / kVec * kVec;
   const int post_gate = f.has_post ? 1 + (f.gate_kind == kGateFeature ? 1 : 0) : 0;
   const Weights<W> wt = {s_w, s_w + ring.weight / sizeof(W), s_w + post_gate * (ring.weight / sizeof(W))};
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
     for (int k = 0; k < kV; ++k)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const int c = column<kA>(threads, k, i);
+        const int c = column<kA>(tid, threads, k, i);
         if (c >= padded) continue;
         const bool in = c < f.cols;
         if (f.has_post) const_cast<W*>(wt.post)[c] = in ? g.post[c] : down<W>(0.f);
@@ -609,11 +617,11 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
   clear(sums);
   bool dead = false;
   float2 stats = both(0.f);
-  if (kGrad && blockIdx.x < f.rows) stats = stats_of(f, blockIdx.x);
-  for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x) {
+  if (kGrad && first < f.rows) stats = stats_of(f, first);
+  for (int64_t row = first; row < f.rows; row += step) {
     const float2 now = stats;
-    if (kGrad && row + gridDim.x < f.rows) stats = stats_of(f, row + gridDim.x);
-    if (!dead && !ptx::mbar_wait(&s_full[s], ph)) {
+    if (kGrad && row + step < f.rows) stats = stats_of(f, row + step);
+    if (!dead && !ptx::mbar_wait(&full[s], ph)) {
       // the outputs are wrong from here; no thread may miss the sums' barriers, so the rows go on without waits
       atomicOr(&g_norm_err, 2u);
       dead = true;
@@ -626,13 +634,13 @@ __global__ void __launch_bounds__(kGrad ? 512 : 1024, 1) rows_kernel(const NormG
     if (f.gate_kind == kGateToken) in.gate = static_cast<const T*>(f.gate) + row * f.ld_gate;
     auto read = [&] {   // this warp has read the stage
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&s_empty[s]);
+      if (lane == 0) ptx::mbar_arrive(&empty[s]);
     };
     if (kGrad)
       row_backward<T, W, kV, kA, true>(a, row, now, in, wt, sum, sums, read);
     else
       row_forward<T, W, kV, kA, true>(f, row, in, wt, sum, read);
-    if (++s == ring.stages) {
+    if (++s == stages) {
       s = 0;
       ph ^= 1;
     }
@@ -674,10 +682,11 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict
 int threads_for(int cols, int v) { return std::max(32, ((cols + kVec - 1) / kVec + v * 32 - 1) / (v * 32) * 32); }
 int vectors(int cols) { return (cols + kVec - 1) / kVec; }
 
-// The persistent kernels' shape with v vectors per thread; false where it does not fit.
-bool ring_shape(const NormArgs& a, bool grad, bool d_out, int v, Ring* ring) {
+// The persistent kernels' shape with v vectors per thread and so many teams; false where it does not fit.
+bool ring_shape(const NormArgs& a, bool grad, bool d_out, int v, int teams, Ring* ring) {
   const int size = type_bytes(a.type), wsize = type_bytes(a.weight_type);
-  const int threads = threads_for(a.cols, v) + 32;
+  const int threads = teams * threads_for(a.cols, v) + 32;
+  ring->teams = teams;
   if (threads > (grad ? 512 : 1024)) return false;
   ring->slot = (a.cols * size + 64 + 127) / 128 * 128;   // up to 15 bytes before the row, and a word behind its last vector
   ring->weight = (a.cols * wsize + 127) / 128 * 128;
@@ -687,8 +696,8 @@ bool ring_shape(const NormArgs& a, bool grad, bool d_out, int v, Ring* ring) {
   // CTAs per SM by registers (64 a thread forward, 128 or less backward) and by shared memory
   for (ring->ctas = std::max(1, std::min(8, (grad && v == 1 ? 640 : grad ? 512 : 1024) / threads)); ring->ctas >= 1; --ring->ctas) {
     const int64_t room = 220 * 1024 / ring->ctas - 2048 - (int64_t)ring->weights * ring->weight;
-    ring->stages = (int)std::min<int64_t>(8, room / (ring->inputs * ring->slot));
-    if (ring->stages >= 2) return true;
+    ring->stages = (int)std::min<int64_t>(8, room / (ring->inputs * ring->slot)) / teams * teams;
+    if (ring->stages >= 2 * teams) return true;
   }
   return false;
 }
@@ -697,31 +706,32 @@ bool ring_shape(const NormArgs& a, bool grad, bool d_out, int v, Ring* ring) {
 // two rows per SM on there is something to bring ahead.  Two vectors per
 // thread leave room for a second CTA on the SM, whose row runs while the first
 // waits at its sums (forward, 4096 x 7168 bf16: 42 us against 54 with one CTA
-// of one; 3584 columns 24 against 29); where its weights do not fit twice, one
-// CTA has more warps with one (fp32 weights: 59 us against 65).
+// of one; 3584 columns 24 against 29); where the weights do not fit twice (fp32,
+// 7168 columns), two teams of threads in one CTA share them.
 int ring_for(const NormArgs& a, bool grad, bool d_out, Ring* ring) {
   const int vecs = vectors(a.cols);
   const bool single = !a.wide && a.type == kF32;
   if (a.rows < 2 * sm_count()) return 0;
   if (grad) {
     // (single accesses with two vectors per thread spill)
-    if (vecs > 64 && !single && ring_shape(a, grad, d_out, 2, ring)) return 2;
-    return (vecs <= 64 || single) && ring_shape(a, grad, d_out, 1, ring) ? 1 : 0;
+    if (vecs > 64 && !single && ring_shape(a, grad, d_out, 2, 1, ring)) return 2;
+    return (vecs <= 64 || single) && ring_shape(a, grad, d_out, 1, 1, ring) ? 1 : 0;
   }
-  if (vecs > 64 && !single && ring_shape(a, grad, d_out, 2, ring) && ring->ctas >= 2) return 2;
-  if (ring_shape(a, grad, d_out, 1, ring)) return 1;
-  return ring_shape(a, grad, d_out, 2, ring) ? 2 : 0;
+  if (vecs > 64 && !single && ring_shape(a, grad, d_out, 2, 1, ring) && ring->ctas >= 2) return 2;
+  if (vecs > 512 && !single && ring_shape(a, grad, d_out, 2, 2, ring)) return 2;
+  if (ring_shape(a, grad, d_out, 1, 1, ring)) return 1;
+  return ring_shape(a, grad, d_out, 2, 1, ring) ? 2 : 0;
 }
 
-template <typename T, typename W, int kV, bool kWide, bool kGrad>
+template <typename T, typename W, int kV, bool kWide, bool kGrad, int kTeams = 1>
 cudaError_t launch_rows(const NormGradArgs& a, const Ring& ring, cudaStream_t st) {
   // rows that are not aligned: 16-bit values by shifted words (4096 x 4567 bf16, backward: 204 us against 376 by single
   // accesses), 32-bit values by single accesses (777 x 1003: 6 us forward against 11 by shifted words)
-  auto* kernel = rows_kernel<T, W, kV, kWide ? kAligned : sizeof(T) == 2 ? kShifted : kStrided, kGrad>;
+  auto* kernel = rows_kernel<T, W, kV, kWide ? kAligned : sizeof(T) == 2 ? kShifted : kStrided, kGrad, kTeams>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring.smem());
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, dim3((unsigned)std::min(a.f.rows, ring.ctas * sm_count())),
-                          dim3(threads_for(a.f.cols, kV) + 32), ring.smem(), st, 1, a, ring);
+                          dim3(ring.teams * threads_for(a.f.cols, kV) + 32), ring.smem(), st, 1, a, ring);
 }
 
 template <typename T, typename W, bool kWide>
@@ -732,7 +742,9 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
   if (vr) {
     NormGradArgs g = {};
     g.f = a;
-    return vr == 1 ? launch_rows<T, W, 1, kWide, false>(g, ring, st) : launch_rows<T, W, 2, kWide, false>(g, ring, st);
+    return ring.teams == 2 ? launch_rows<T, W, 2, kWide, false, 2>(g, ring, st)
+           : vr == 1       ? launch_rows<T, W, 1, kWide, false>(g, ring, st)
+                           : launch_rows<T, W, 2, kWide, false>(g, ring, st);
   }
   const int vecs = vectors(a.cols);
   const int v = vecs <= 1024 ? 1 : 4;
