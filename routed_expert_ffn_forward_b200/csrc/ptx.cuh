@@ -177,6 +177,11 @@ __device__ __forceinline__ void bulk_load_hint(void* smem_dst, const void* src, 
                : "memory");
 }
 
+// Bring bytes into L2 (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
+}
+
 // ---- programmatic dependent launch --------------------------------------------
 // Wait until the grids this one depends on have completed and their memory is visible.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
