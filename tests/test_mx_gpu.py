@@ -265,3 +265,31 @@ def test_product_on_a_side_stream_and_in_a_graph():
         x.copy_(xs[i])
         graph.replay()
         assert torch.equal(out, want[i])
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+from routed_expert_ffn_forward_b200 import block
+g = torch.Generator(device="cuda").manual_seed(5)
+x = block.mx_quantize(torch.randn(1, 7168, device="cuda", generator=g))
+w = block.mx_pack(block.mx_quantize(torch.randn(512, 7168, device="cuda", generator=g)))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = block.mx_product(x, w, out_dtype=torch.float32)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(got, block.mx_product(x, w, out_dtype=torch.float32))
+block.check()
+print("same")
+"""
+
+
+def test_first_product_of_a_process_is_captured():
+    """What the split of K asks of the device once, it may ask during a capture."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], capture_output=True, text=True, timeout=300,
+                          cwd=Path(__file__).resolve().parents[1])
+    assert done.returncode == 0 and done.stdout.strip() == "same", done.stdout + done.stderr
