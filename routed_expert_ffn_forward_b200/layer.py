@@ -116,9 +116,14 @@ class MoELayer:
         """The layer's forward over the MXFP4 products (see ``moe_forward_mx``)."""
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.H or not x.is_contiguous():
             raise ValueError(f"x must be contiguous bfloat16 [T, {self.H}], not {x.dtype} {tuple(x.shape)}")
+        if x.device.type != "cuda":
+            raise ValueError(f"x must be on a GPU, not on {x.device}")
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device)
+        elif out.dtype != x.dtype or out.shape != x.shape or out.device != x.device or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous bfloat16 {tuple(x.shape)} on {x.device}, "
+                             f"not {out.dtype} {tuple(out.shape)} on {out.device}")
         s = stream if stream is not None else torch.cuda.current_stream().cuda_stream
         moe.moe_forward_mx(self.handle, x.data_ptr(), out.data_ptr(), T, s)
         return out

@@ -127,6 +127,30 @@ def test_forward_mx_refusals_without_a_layer():
     refused(BAD, moe.moe_set_mx_experts, None, P, P)
 
 
+def bare_layer(**attrs):
+    """A MoELayer without a library layer, for checks that come before its use."""
+    from routed_expert_ffn_forward_b200.layer import MoELayer
+    L = MoELayer.__new__(MoELayer)
+    L.E, L.S, L.H, L.I, L.k, L.handle = 4, 0, 256, 128, 2, None
+    for name, value in attrs.items():
+        setattr(L, name, value)
+    return L
+
+
+def test_forward_mx_tensor_checks():
+    L, bf = bare_layer(), torch.bfloat16
+    x = torch.zeros((4, 256), dtype=bf)
+    meta = torch.zeros((4, 256), dtype=bf, device="meta")
+    for call in (
+        lambda: L.forward_mx(x),                                             # not on a GPU
+        lambda: L.forward_mx(meta),
+        lambda: L.forward_mx(x.float()),
+        lambda: L.forward_mx(x[:, :128]),
+    ):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_tensor_checks():
     bf, f32 = torch.bfloat16, torch.float32
     x, w = torch.zeros((4, 64), dtype=bf), torch.ones(64, dtype=bf)

@@ -134,6 +134,10 @@ def test_forward_mx_refusals(layer):
         L.set_mx_experts(L.mx[1], L.mx[0])
     with pytest.raises(ValueError):
         L.forward_mx(torch.zeros((L.H, 4), device="cuda", dtype=torch.bfloat16).t())
+    x = torch.zeros((4, L.H), device="cuda", dtype=torch.bfloat16)
+    for out in (x[:3].clone(), x.float(), x.cpu(), torch.zeros((4, 2 * L.H), device="cuda", dtype=torch.bfloat16)[:, ::2]):
+        with pytest.raises(ValueError):
+            L.forward_mx(x, out=out)
     from routed_expert_ffn_forward_b200.layer import MoELayer
     M = MoELayer(256, 128, 4, 2, 0)
     try:
