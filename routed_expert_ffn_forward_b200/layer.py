@@ -97,6 +97,10 @@ class MoELayer:
             if (w.n_mats, w.rows, w.cols, w.paired) != shape:
                 raise ValueError(f"{name} must be {shape} (n_mats, rows, cols, paired), "
                                  f"not {(w.n_mats, w.rows, w.cols, w.paired)}")
+            size = moe.moe_mx_image_bytes(w.n_mats, w.rows, w.cols)
+            if w.image.device.type != "cuda" or w.image.dtype != torch.uint8 or w.image.numel() != size:
+                raise ValueError(f"{name}'s image must be {size} bytes on a GPU, "
+                                 f"not {w.image.dtype} [{w.image.numel()}] on {w.image.device}")
         moe.moe_set_mx_experts(self.handle, gate_up.image.data_ptr(), down.image.data_ptr())
         self.mx = (gate_up, down)            # the library borrows the images
 

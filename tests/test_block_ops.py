@@ -141,11 +141,16 @@ def test_forward_mx_tensor_checks():
     L, bf = bare_layer(), torch.bfloat16
     x = torch.zeros((4, 256), dtype=bf)
     meta = torch.zeros((4, 256), dtype=bf, device="meta")
+    gate_up = block.MXWeights(torch.zeros(4 * 34816, dtype=torch.uint8), 4, 256, 256, True)
+    down = block.MXWeights(torch.zeros(4 * 34816, dtype=torch.uint8), 4, 256, 128, False)
     for call in (
         lambda: L.forward_mx(x),                                             # not on a GPU
         lambda: L.forward_mx(meta),
         lambda: L.forward_mx(x.float()),
         lambda: L.forward_mx(x[:, :128]),
+        lambda: L.set_mx_experts(gate_up, down),                             # not on a GPU
+        lambda: L.set_mx_experts(gate_up._replace(paired=False), down),
+        lambda: L.set_mx_experts(gate_up._replace(cols=128), down),
     ):
         with pytest.raises(ValueError):
             call()

@@ -132,6 +132,9 @@ def test_forward_mx_refusals(layer):
     assert e.value.status == moe.MOE_ERR_INVALID_ARG
     with pytest.raises(ValueError):
         L.set_mx_experts(L.mx[1], L.mx[0])
+    for image in (L.mx[0].image[:-34816], L.mx[0].image.cpu()):
+        with pytest.raises(ValueError):
+            L.set_mx_experts(L.mx[0]._replace(image=image), L.mx[1])
     with pytest.raises(ValueError):
         L.forward_mx(torch.zeros((L.H, 4), device="cuda", dtype=torch.bfloat16).t())
     x = torch.zeros((4, L.H), device="cuda", dtype=torch.bfloat16)
