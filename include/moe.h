@@ -303,6 +303,12 @@ moe_status moe_get_routing(moe_layer_t layer, int32_t* ids, float* weights, void
  * counterpart on the pages (inspection). */
 moe_status moe_get_logits(moe_layer_t layer, float* logits, void* stream);
 
+/* Tokens of the last forward, which moe_get_routing and moe_get_logits copy:
+ * 0 before the first (a forward of no tokens changes nothing) and for a null
+ * layer.  Host state: a replayed graph does not set it.  No counterpart on the
+ * pages (inspection). */
+int moe_last_tokens(moe_layer_t layer);
+
 /* Streaming mode: start fetching the given experts (host array of n ids in
  * 0..E+S-1) into the cache now, on the copy stream, so a later forward finds
  * them ready.  A no-op for resident layers and for experts already cached.

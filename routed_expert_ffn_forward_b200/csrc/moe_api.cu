@@ -1389,6 +1389,8 @@ moe_status moe_get_logits(moe_layer_t L, float* logits, void* stream) {
   return MOE_OK;
 }
 
+int moe_last_tokens(moe_layer_t L) { return L ? L->last_T : 0; }
+
 moe_status moe_prefetch(moe_layer_t L, const int32_t* ids, int n) {
   g_err.clear();
   if (!L || (n > 0 && !ids) || n < 0) return fail(MOE_ERR_INVALID_ARG, "bad argument");

@@ -155,9 +155,16 @@ class MoELayer:
                      mask: Optional[torch.Tensor] = None):
         """Balance loss of the last forward's routing (T tokens), its per-expert
         counts and the gradient of the router's logits: (loss, counts [seqs, E],
-        d_logits [T, E]); see ``block.balance_loss``."""
-        logits = self.logits(T)
-        loss, counts, slope = block.balance_loss_forward(logits, self.routing(T)[0], coef, self.gating, offsets, mask)
+        d_logits [T, E]); see ``block.balance_loss``.  T is that forward's, or 0."""
+        last = moe.moe_last_tokens(self.handle)
+        if T not in (0, last):   # the library copies as many rows as that forward had
+            raise ValueError(f"T={T}, but the last forward had {last} tokens")
+        if T:
+            logits, ids = self.logits(T), self.routing(T)[0]
+        else:
+            logits = torch.empty((0, self.E), dtype=torch.float32, device="cuda")
+            ids = torch.empty((0, self.k), dtype=torch.int32, device="cuda")
+        loss, counts, slope = block.balance_loss_forward(logits, ids, coef, self.gating, offsets, mask)
         return loss, counts, block.balance_loss_backward(None, slope, logits, self.gating, offsets, mask)
 
     def routing(self, T: int):

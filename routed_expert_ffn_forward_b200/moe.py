@@ -46,7 +46,7 @@ SIZE_MAX = (1 << 64) - 1
 # every entry point declared in include/moe.h
 EXPORTS = ("moe_expert_bytes", "moe_layer_create", "moe_layer_create_mixed", "moe_layer_destroy", "moe_set_router",
            "moe_set_experts", "moe_set_cache_bytes", "moe_set_cache_policy", "moe_set_few_row_tiles", "moe_forward", "moe_forward_routed",
-           "moe_forward_host", "moe_get_routing", "moe_get_logits", "moe_prefetch",
+           "moe_forward_host", "moe_get_routing", "moe_get_logits", "moe_last_tokens", "moe_prefetch",
            "moe_check", "moe_get_stats", "moe_reset_stats", "moe_set_profiling", "moe_get_profile",
            "moe_reset_profile", "moe_route_noalloc", "moe_set_test_hooks", "moe_set_expert_parallel",
            "moe_forward_partial", "moe_combine_partials", "moe_mx_quantize", "moe_mx_image_bytes", "moe_mx_pack",
@@ -123,6 +123,7 @@ def lib() -> ctypes.CDLL:
             "moe_forward_host": (_I, [_P, _P, _P, _I, _P]),
             "moe_get_routing": (_I, [_P, _P, _P, _P]),
             "moe_get_logits": (_I, [_P, _P, _P]),
+            "moe_last_tokens": (_I, [_P]),
             "moe_prefetch": (_I, [_P, _P, _I]),
             "moe_check": (_I, [_P]),
             "moe_get_stats": (_I, [ctypes.POINTER(moe_stats)]),
@@ -232,6 +233,10 @@ def moe_get_routing(layer: int, ids: int | None, weights: int | None, stream: in
 
 def moe_get_logits(layer: int, logits: int, stream: int | None = None) -> None:
     _check(lib().moe_get_logits(layer, logits, stream or None))
+
+
+def moe_last_tokens(layer: int) -> int:
+    return int(lib().moe_last_tokens(layer))
 
 
 def moe_prefetch(layer: int, ids_host: int, n: int) -> None:

@@ -156,6 +156,16 @@ def test_forward_mx_tensor_checks():
             call()
 
 
+def test_balance_loss_of_another_number_of_tokens(monkeypatch):
+    """Routing and logits are copied for the last forward's tokens, whatever the
+    tensors hold: another T is refused before anything is allocated."""
+    assert moe.moe_last_tokens(None) == 0
+    monkeypatch.setattr(moe, "moe_last_tokens", lambda handle: 8)
+    for T in (7, 9, -1):
+        with pytest.raises(ValueError, match="the last forward had 8"):
+            bare_layer(gating=1).balance_loss(T, 0.01)
+
+
 def test_tensor_checks():
     bf, f32 = torch.bfloat16, torch.float32
     x, w = torch.zeros((4, 64), dtype=bf), torch.ones(64, dtype=bf)

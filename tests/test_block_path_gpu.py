@@ -193,6 +193,11 @@ def test_block_and_balance_loss(layer, T, mx):
     want, c = block_ref.balance_loss(leaf, ids.cpu(), 0.01, True)
     dw = torch.autograd.grad(want, leaf)[0]
     assert torch.equal(counts.cpu(), c) and int(counts.sum()) == T * L.k
+    assert moe.moe_last_tokens(L.handle) == T
+    with pytest.raises(ValueError):
+        L.balance_loss(T + 1, 0.01)
+    nothing = L.balance_loss(0, 0.01)
+    assert float(nothing[0]) == 0 and int(nothing[1].sum()) == 0 and nothing[2].shape == (0, L.E)
     assert abs(float(loss) - float(want)) <= 1e-5 * float(want)
     assert bool(((f(d_logits) - dw).abs() <= 4e-5 * dw.abs().max()).all())
     with pytest.raises(ValueError):
