@@ -107,11 +107,16 @@ moe_status norm_args(const moe_norm_args* p, bool grad, NormArgs* a) {
   a->has_post = post;
   a->scale = p->scale;
   a->eps = p->eps;
-  auto vec = [](const void* q, int64_t ld) { return aligned(q, 16) && ld % 8 == 0; };
-  a->wide = p->cols % 8 == 0 && vec(p->h, p->ld_h) && aligned(p->post, 16) && aligned(p->pre, 16) &&
-            (!post || vec(p->y, p->ld_y)) && (p->gate_kind != MOE_GATE_FULL || vec(p->gate, p->ld_gate)) &&
-            (p->gate_kind != MOE_GATE_FEATURE || aligned(p->gate, 16)) &&
-            (grad || ((!post || vec(p->out, p->ld_out)) && (!pre || vec(p->next, p->ld_next))));
+  // accesses of n values: 8 in 16-byte words, or 2
+  auto every = [&](int n, size_t row_align, size_t weight_align) {
+    auto fits = [&](const void* q, int64_t ld) { return aligned(q, row_align) && ld % n == 0; };
+    return p->cols % n == 0 && fits(p->h, p->ld_h) && aligned(p->post, weight_align) && aligned(p->pre, weight_align) &&
+           (!post || fits(p->y, p->ld_y)) && (p->gate_kind != MOE_GATE_FULL || fits(p->gate, p->ld_gate)) &&
+           (p->gate_kind != MOE_GATE_FEATURE || aligned(p->gate, weight_align)) &&
+           (grad || ((!post || fits(p->out, p->ld_out)) && (!pre || fits(p->next, p->ld_next))));
+  };
+  a->wide = every(8, 16, 16);
+  a->even = every(2, 2 * t, 2 * w);
   return MOE_OK;
 }
 
@@ -259,10 +264,13 @@ moe_status moe_block_norm_grad(const moe_norm_args* args, const moe_norm_grads* 
   a.partial = static_cast<float*>(workspace);
   a.n_parts = 0;   // the launcher's choice, at most what the workspace holds
   a.n_sums = (post ? 1 : 0) + (pre ? 1 : 0) + (f.gate_kind == MOE_GATE_FEATURE ? 1 : 0);
-  auto vec = [](const void* q, int64_t ld) { return aligned(q, 16) && ld % 8 == 0; };
-  a.f.wide = f.wide && vec(g->d_h, g->ld_d_h) && (!g->d_out || vec(g->d_out, g->ld_d_out)) &&
-             (!pre || vec(g->d_next, g->ld_d_next)) && (!post || vec(g->d_y, g->ld_d_y)) &&
-             (f.gate_kind != MOE_GATE_FULL || vec(g->d_gate, g->ld_d_gate));
+  auto every = [&](int n, size_t align) {
+    auto fits = [&](const void* q, int64_t ld) { return aligned(q, align) && ld % n == 0; };
+    return fits(g->d_h, g->ld_d_h) && (!g->d_out || fits(g->d_out, g->ld_d_out)) && (!pre || fits(g->d_next, g->ld_d_next)) &&
+           (!post || fits(g->d_y, g->ld_d_y)) && (f.gate_kind != MOE_GATE_FULL || fits(g->d_gate, g->ld_d_gate));
+  };
+  a.f.wide = f.wide && every(8, 16);
+  a.f.even = f.even && every(2, 2 * t);
   return launched(launch_norm_grad(a, static_cast<cudaStream_t>(stream)), 2, "block norm gradient");
 }
 

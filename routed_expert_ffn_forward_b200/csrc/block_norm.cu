@@ -95,6 +95,9 @@ struct Packed<float> {
     return {{make_float2(f[0].x, f[0].y), make_float2(f[0].z, f[0].w), make_float2(f[1].x, f[1].y),
              make_float2(f[1].z, f[1].w)}};
   }
+  using Pair = float2;
+  static __device__ __forceinline__ float2 unpack2(float2 w) { return w; }
+  static __device__ __forceinline__ float2 pack2(float2 v) { return v; }
   static __device__ __forceinline__ void pack(const V8& v, uint4* w) {
     float4* f = reinterpret_cast<float4*>(w);
     f[0] = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
@@ -108,6 +111,9 @@ struct Packed<__half> {
     const __half2* h = reinterpret_cast<const __half2*>(w);
     return {{__half22float2(h[0]), __half22float2(h[1]), __half22float2(h[2]), __half22float2(h[3])}};
   }
+  using Pair = __half2;
+  static __device__ __forceinline__ float2 unpack2(__half2 w) { return __half22float2(w); }
+  static __device__ __forceinline__ __half2 pack2(float2 v) { return __float22half2_rn(v); }
   static __device__ __forceinline__ void pack(const V8& v, uint4* w) {
     __half2* h = reinterpret_cast<__half2*>(w);
 #pragma unroll
@@ -121,6 +127,9 @@ struct Packed<__nv_bfloat16> {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
   static __device__ __forceinline__ V8 unpack(const uint4* w) { return {{two(w->x), two(w->y), two(w->z), two(w->w)}}; }
+  using Pair = __nv_bfloat162;
+  static __device__ __forceinline__ float2 unpack2(__nv_bfloat162 w) { return two(*reinterpret_cast<const uint32_t*>(&w)); }
+  static __device__ __forceinline__ __nv_bfloat162 pack2(float2 v) { return __float22bfloat162_rn(v); }
   static __device__ __forceinline__ void pack(const V8& v, uint4* w) {
     __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(w);
 #pragma unroll
@@ -131,14 +140,18 @@ struct Packed<__nv_bfloat16> {
 // How rows are accessed.  kAligned: cols and row strides multiples of 8, bases
 // aligned to 16 bytes.  kShifted: rows at any offset, read from a copy in
 // shared memory at the same offset from a 16-byte boundary and stored in whole
-// 16-byte words, both by shifting across word borders.  kStrided: single accesses.
-enum Access { kStrided, kAligned, kShifted };
+// 16-byte words, both by shifting across word borders.  kPairs: cols and row
+// strides even, bases aligned to two values, accesses of two.  kStrided: of one.
+enum Access { kStrided, kPairs, kAligned, kShifted };
 
 // The eight columns of vector k of this thread: consecutive ones, or with
-// kStrided every threads-th, so that a warp's single accesses stay side by side.
+// kPairs and kStrided every threads-th pair or value, so that a warp's accesses
+// stay side by side.
 template <Access kA>
 __device__ __forceinline__ int column(int tid, int threads, int k, int i) {
-  return kA != kStrided ? (tid + k * threads) * kVec + i : tid + (k * kVec + i) * threads;
+  return kA == kStrided ? tid + (k * kVec + i) * threads
+         : kA == kPairs ? 2 * (tid + (k * (kVec / 2) + i / 2) * threads) + i % 2
+                        : (tid + k * threads) * kVec + i;
 }
 // A row's columns, the threads that share them and this one's number among them.
 struct Span {
@@ -157,6 +170,14 @@ __device__ __forceinline__ V8 load8(const T* row, int k, const Span& sp) {
     for (int i = 0; i < kVec; ++i) {
       const int c = column<kStrided>(sp.tid, sp.threads, k, i);
       if (c < sp.cols) v.set(i, up(row[c]));
+    }
+    return v;
+  }
+  if (kA == kPairs) {
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) {
+      const int c = column<kPairs>(sp.tid, sp.threads, k, 2 * i);
+      if (c < sp.cols) v.p[i] = Packed<T>::unpack2(*reinterpret_cast<const typename Packed<T>::Pair*>(row + c));
     }
     return v;
   }
@@ -192,6 +213,14 @@ __device__ __forceinline__ void store8(T* row, int k, const Span& sp, const V8& 
     for (int i = 0; i < kVec; ++i) {
       const int c = column<kStrided>(sp.tid, sp.threads, k, i);
       if (c < sp.cols) row[c] = down<T>(v.get(i));
+    }
+    return;
+  }
+  if (kA == kPairs) {
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) {
+      const int c = column<kPairs>(sp.tid, sp.threads, k, 2 * i);
+      if (c < sp.cols) *reinterpret_cast<typename Packed<T>::Pair*>(row + c) = Packed<T>::pack2(v.p[i]);
     }
     return;
   }
@@ -440,7 +469,7 @@ __device__ __forceinline__ void row_backward(const NormGradArgs& a, int64_t row,
 template <typename W, int kV, Access kA, bool kShared>
 __device__ __forceinline__ void store_sums(const NormGradArgs& a, const Weights<W>& wt, const ColumnSums<kV>& s,
                                            int threads) {
-  constexpr Access kSumAccess = kA == kStrided ? kStrided : kAligned;   // the partial rows are padded to whole vectors
+  constexpr Access kSumAccess = kA == kShifted ? kAligned : kA;   // the partial rows are padded to whole vectors
   const Span sp = {a.f.cols, threads, (int)threadIdx.x};
   const int64_t padded = (sp.cols + 7) / 8 * 8;
   float* p = a.partial + (int64_t)blockIdx.x * a.n_sums * padded;
@@ -725,9 +754,15 @@ int ring_for(const NormArgs& a, bool grad, bool d_out, Ring* ring) {
 
 template <typename T, typename W, int kV, bool kWide, bool kGrad, int kTeams = 1>
 cudaError_t launch_rows(const NormGradArgs& a, const Ring& ring, cudaStream_t st) {
-  // rows that are not aligned: 16-bit values by shifted words (4096 x 4567 bf16, backward: 204 us against 376 by single
-  // accesses), 32-bit values by single accesses (777 x 1003: 6 us forward against 11 by shifted words)
-  auto* kernel = rows_kernel<T, W, kV, kWide ? kAligned : sizeof(T) == 2 ? kShifted : kStrided, kGrad, kTeams>;
+  // Rows that are not aligned.  16-bit values: by pairs where all rows start at one, else by shifted words (neighbouring
+  // widths, pairs against words: 16384 x 1002 bf16 forward 45 us, 1001 87, backward 141 against 199; 4096 x 7166 fp16
+  // 76 against 113, 205 against 214; words against single accesses, 4096 x 4567 backward: 204 against 376).  32-bit
+  // values: by single accesses (777 x 1003: 6 us forward against 11 by shifted words; 3000 x 2998 backward 80 us,
+  // by pairs 124).
+  constexpr Access kOther = sizeof(T) == 2 ? kShifted : kStrided, kEven = sizeof(T) == 2 ? kPairs : kOther;
+  auto* kernel = kWide      ? rows_kernel<T, W, kV, kAligned, kGrad, kTeams>
+                 : a.f.even ? rows_kernel<T, W, kV, kEven, kGrad, kTeams>
+                            : rows_kernel<T, W, kV, kOther, kGrad, kTeams>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring.smem());
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, dim3((unsigned)std::min(a.f.rows, ring.ctas * sm_count())),

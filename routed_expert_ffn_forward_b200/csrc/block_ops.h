@@ -104,6 +104,7 @@ struct NormArgs {
   int rows, cols, type, weight_type, gate_kind;
   float scale, eps;
   bool has_post;                           // a norm of y (y is null without rows)
+  bool even;                               // accesses of two values: cols and every ld even, bases aligned to two
   bool wide;                               // 16-byte accesses: cols and every ld a multiple of 8, bases aligned
 };
 struct NormGradArgs {
