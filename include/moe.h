@@ -480,9 +480,10 @@ typedef struct {
   float scale, eps;
 } moe_norm_args;
 /* Gradients, each of the type and shape of what it is the gradient of; d_h
- * includes the residual path.  d_out NULL: zeros.  d_y and d_post only with
- * post, d_next and d_pre only with pre, d_gate only with a gate (summed over
- * the rows for MOE_GATE_FEATURE, over the columns for MOE_GATE_TOKEN). */
+ * includes the residual path.  d_out NULL: zeros.  d_next is given with pre
+ * and NULL without it.  d_y and d_post are written only with post, d_pre only
+ * with pre, d_gate only with a gate (summed over the rows for
+ * MOE_GATE_FEATURE, over the columns for MOE_GATE_TOKEN). */
 typedef struct {
   const void *d_out, *d_next;
   void *d_h, *d_y, *d_post, *d_gate, *d_pre;

@@ -237,6 +237,8 @@ moe_status moe_block_norm_grad(const moe_norm_args* args, const moe_norm_grads* 
   if ((rows && (!g->d_h || (post && !g->d_y) || (pre && !g->d_next))) || (post && !g->d_post) || (pre && !g->d_pre) ||
       (gate && !g->d_gate && (rows || f.gate_kind == MOE_GATE_FEATURE)) || !workspace)
     return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  // the kernels bring every input that is there into a stage that holds what pre and post ask for
+  if (!pre && g->d_next) return fail(MOE_ERR_INVALID_ARG, "d_next without pre weights");
   if ((g->d_out && g->ld_d_out < f.cols) || g->ld_d_h < f.cols || (pre && g->ld_d_next < f.cols) ||
       (post && g->ld_d_y < f.cols) || (f.gate_kind == MOE_GATE_FULL && g->ld_d_gate < f.cols) ||
       (f.gate_kind == MOE_GATE_TOKEN && g->ld_d_gate < 1))

@@ -103,6 +103,17 @@ def test_norm_gradient_refusals():
     assert moe.lib().moe_block_norm(None, None) == BAD
 
 
+@pytest.mark.parametrize("rows", [0, 4, 3000])
+def test_norm_gradient_of_an_output_that_is_not_there(rows):
+    """Without pre there is no next, and a gradient of it is refused at any number
+    of rows (a stage of the ring has no room for it)."""
+    size = moe.moe_block_norm_workspace(rows, 64)
+    g = dict(d_out=P, d_h=P, d_y=P, d_post=P, d_gate=P, ld_d_out=64, ld_d_h=64, ld_d_y=64, ld_d_gate=64)
+    for ld in (0, 64):
+        refused(BAD, moe.moe_block_norm_grad, norm(rows=rows, pre=None, next=None),
+                moe.moe_norm_grads(d_next=P, ld_d_next=ld, **g), P, size)
+
+
 def test_balance_refusals():
     size = moe.moe_balance_workspace(64, 16, 1)
     assert size > 0
