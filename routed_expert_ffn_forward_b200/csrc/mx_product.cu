@@ -295,6 +295,15 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
     ptx::cluster_sync();   // the barriers of both CTAs are set up
   }
   const int k0 = kSplit ? a.kc * rank / cluster : 0, k1 = kSplit ? a.kc * (rank + 1) / cluster : a.kc;
+  // Waits for the arrivals of the MMAs' commits on this CTA's barriers: of the last stages (`it` were consumed), which
+  // no copy waits for any more, and of the drain behind them.  A pair's first CTA commits for both, and its arrivals
+  // in the second are ordered by nothing else: one that came late would land in shared memory of the next CTA there.
+  auto settle = [&](int it, uint64_t limit_ns) {
+    bool ok = true;
+    for (int i = max(it - kNS, 0); i < it; ++i) ok = ptx::mbar_wait(&empty[i % kNS], (i / kNS) & 1, limit_ns) && ok;
+    return ptx::mbar_wait(drain, 0, limit_ns) && ok;
+  };
+  constexpr uint64_t kWait = 2000000000ull;
 
   if (warp < kRowWarps) {
     // ------------------------------------------------------------ rows of x
@@ -405,6 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
           ptx::fence_proxy_async();
           ptx::mbar_arrive_cluster(&peer_full[s], 0);
         }
+      // (the first CTA may have to give up on waits of its own before its last commit)
+      if (!settle(it, 4 * kWait)) atomicOr(&g_mx_err, 16u);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA (the whole warp; one lane's instructions)
@@ -412,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
     const uint32_t ring = ptx::smem_u32(sm);
     using S = Slots<C, kNAcc, kTwo>;
     S slots;
-    int s = 0, n = 0;
+    int s = 0, n = 0, it = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int u; ok && (u = unit_of(n)) < n_units; ++n) {
@@ -448,6 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
           ptx::umma_mxf4<kTwo>(on, d1, wd + kMxHalfCodes / 16 + 2 * q, rd + 2 * q, id, tmem + C::kSA + 8 + 4 * c, sb, add);
         }
         ptx::umma_commit_on<kTwo>(on, &empty[s]);
+        ++it;
         if (++s == kNS) {
           s = 0;
           ph ^= 1;
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
     }
     // wait for every MMA this warp issued before TMEM is released
     ptx::umma_commit_on<kTwo>(on, drain);
-    if (!ptx::mbar_wait(drain, 0) && on) atomicOr(&g_mx_err, 4u);
+    if (!settle(it, kWait) && on) atomicOr(&g_mx_err, 4u);
   } else if (warp >= kFirstEpi) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, sub = (warp - kFirstEpi) >> 2;   // TMEM lane quarter; which 16-column chunks
