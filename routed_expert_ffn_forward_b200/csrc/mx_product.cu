@@ -487,7 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
       const typename S::Plan pl = slots.next(un.count);
       const bool behind = kTwo && 2 * un.row_tile + rank >= a.row_tiles;
       const Store<kPaired, Out> store(a, row_tile_of(un) * 128 + lrow);
-      ok = ptx::mbar_wait_sleep(&acc_full[pl.slot], pl.use0, 100);
+      // (both slots of a whole unit: the second one's parity is asked again by the unit after next, and a phase that had
+      // not ended by then would look like the one before it)
+      ok = ptx::mbar_wait_sleep(&acc_full[pl.slot], pl.use0, 100) &&
+           (!pl.whole || ptx::mbar_wait_sleep(&acc_full[1], pl.use1, 100));
       __syncwarp();
       if (!ok) {
         atomicOr(&g_mx_err, 8u);

@@ -40,6 +40,8 @@ def mixed_counts(n, seed):
 # pairs: 9 row tiles are 5 pairs of tiles, of 54 tiles of rows and more: 270 units and more for 74 pairs;
 # one CTA each: 38 tiles of rows and more, of 9 row tiles: 342 units and more for 148
 CASES = [("pairs", mixed_counts(40, 1), 2050, 544), ("pairs", mixed_counts(44, 2), 2306, 200),
+         # accumulators that take both slots and one slot in turn, with one step each
+         ("pairs", [240, 112, 240, 16, 112] * 12, 1026, 96),
          ("single", [25] * 36 + [64, 36, 0], 2050, 544), ("single", [65, 16, 1, 300, 0, 128] + [7] * 30, 2306, 1500)]
 
 
