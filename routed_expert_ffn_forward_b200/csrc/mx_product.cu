@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
         store.one(store.base + (un.row0 + c) * store.ld, v0, v1);
       }
     }
+    __syncwarp();          // the rows' loop leaves a warp's lanes apart, and the barrier takes whole warps
     ptx::cluster_sync();   // no CTA leaves while its part is read
   }
   if (warp == kMmaWarp) {

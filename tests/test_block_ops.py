@@ -133,6 +133,22 @@ def test_balance_refusals():
         refused(BAD, moe.moe_balance_loss_grad, *{**grad, **changes}.values())
 
 
+def test_cluster_barriers_are_reached_by_whole_warps():
+    """The aligned cluster barrier is undefined for a warp whose lanes are apart:
+    every use follows a __syncwarp() directly."""
+    import os
+    csrc = os.path.join(os.path.dirname(build.__file__), "csrc")
+    uses = 0
+    for path in build.sources():
+        lines = [l.split("//")[0].strip() for l in open(path)]
+        lines = [l for l in lines if l]
+        for before, line in zip(lines, lines[1:]):
+            if "cluster_sync()" in line:
+                uses += 1
+                assert before == "__syncwarp();", (os.path.relpath(path, csrc), before, line)
+    assert uses >= 4
+
+
 def test_forward_mx_refusals_without_a_layer():
     refused(BAD, moe.moe_forward_mx, None, P, P, 4)
     refused(BAD, moe.moe_set_mx_experts, None, P, P)
