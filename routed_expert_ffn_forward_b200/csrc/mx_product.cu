@@ -151,6 +151,10 @@ struct Slots {
 // silu(gate) * up, ~1e-6 relative
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
+// What a lane's bounded wait found, as one answer of the warp: lanes that went on while others gave up would wait for
+// them at the next shuffle or tensor-memory load without a bound.
+__device__ __forceinline__ bool warp_agrees(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 // Where a thread's accumulators go: lane i of the unit's 128, two accumulators
 // each (features 2 i and 2 i + 1, or the gate and up of feature i).
 template <bool kPaired, typename Out>
@@ -433,10 +437,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
       constexpr int kM = kTwo ? 256 : 128;
       const uint32_t id0 = ptx::umma_idesc_mxf4(kM, N, 0), id1 = ptx::umma_idesc_mxf4(kM, N, 1);
       const uint32_t d0 = tmem + C::column(slot, 0), d1 = tmem + C::column(slot, 1);
-      ok = ptx::mbar_wait(&acc_empty[slot], pl.use0 ^ 1) && (!pl.whole || ptx::mbar_wait(&acc_empty[1], pl.use1 ^ 1));
+      ok = warp_agrees(ptx::mbar_wait(&acc_empty[slot], pl.use0 ^ 1) &&
+                       (!pl.whole || ptx::mbar_wait(&acc_empty[1], pl.use1 ^ 1)));
       ptx::tc_fence_after();
       for (int k = k0; k < k1 && ok; ++k) {
-        ok = ptx::mbar_wait(&full[s], ph) && (!kTwo || ptx::mbar_wait(&peer_full[s], ph));
+        ok = warp_agrees(ptx::mbar_wait(&full[s], ph) && (!kTwo || ptx::mbar_wait(&peer_full[s], ph)));
         if (!ok) break;
         ptx::fence_proxy_async();   // the rows came through the generic proxy
         ptx::tc_fence_after();
@@ -489,9 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
       const Store<kPaired, Out> store(a, row_tile_of(un) * 128 + lrow);
       // (both slots of a whole unit: the second one's parity is asked again by the unit after next, and a phase that had
       // not ended by then would look like the one before it)
-      ok = ptx::mbar_wait_sleep(&acc_full[pl.slot], pl.use0, 100) &&
-           (!pl.whole || ptx::mbar_wait_sleep(&acc_full[1], pl.use1, 100));
-      __syncwarp();
+      ok = warp_agrees(ptx::mbar_wait_sleep(&acc_full[pl.slot], pl.use0, 100) &&
+                       (!pl.whole || ptx::mbar_wait_sleep(&acc_full[1], pl.use1, 100)));
       if (!ok) {
         atomicOr(&g_mx_err, 8u);
         break;

@@ -149,6 +149,21 @@ def test_cluster_barriers_are_reached_by_whole_warps():
     assert uses >= 4
 
 
+def test_warps_that_stay_together_give_up_together():
+    """The product's MMA and epilogue warps shuffle and load tensor memory as whole
+    warps, so each of their bounded waits ends with one answer of the warp."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(build.__file__), "csrc", "mx_product.cu")).read()
+    mma = text.index("- MMA (the whole warp")
+    epilogue = text.index("- epilogue\n", mma)
+    end = text.index("__syncthreads()", epilogue)
+    roles = re.sub(r"//[^\n]*", "", text[mma:end])
+    waits = [m.start() for m in re.finditer(r"mbar_wait", roles)]
+    agreed = [i for m in re.finditer(r"warp_agrees\((.*?)\);", roles, re.S) for i in range(m.start(), m.end())]
+    assert len(waits) >= 6 and set(waits) <= set(agreed)
+
+
 def test_forward_mx_refusals_without_a_layer():
     refused(BAD, moe.moe_forward_mx, None, P, P, 4)
     refused(BAD, moe.moe_set_mx_experts, None, P, P)
