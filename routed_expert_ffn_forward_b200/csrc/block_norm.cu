@@ -540,6 +540,11 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(const NormGradArgs a) {
 // bit flags: a bounded wait that gave up
 __device__ unsigned g_norm_err = 0;
 
+// The most dynamic shared memory of a ring (ring_shape).  Every launch allows its
+// kernel this much: the limit belongs to the kernel, not to the launch, and one
+// that followed a call's own size could shrink below another thread's launch.
+constexpr int kRingSmem = 220 * 1024 - 2048;
+
 struct Ring {
   int teams;                  // of threads in a CTA, each with rows and stages of its own
   int stages, inputs, slot;   // stages (of all teams) of so many input rows of `slot` bytes
@@ -724,7 +729,7 @@ bool ring_shape(const NormArgs& a, bool grad, bool d_out, int v, int teams, Ring
   ring->weights = (a.has_post ? 1 : 0) + (a.gate_kind == kGateFeature ? 1 : 0) + (a.pre ? 1 : 0);
   // CTAs per SM by registers (64 a thread forward, 128 or less backward) and by shared memory
   for (ring->ctas = std::max(1, std::min(8, (grad && v == 1 ? 640 : grad ? 512 : 1024) / threads)); ring->ctas >= 1; --ring->ctas) {
-    const int64_t room = 220 * 1024 / ring->ctas - 2048 - (int64_t)ring->weights * ring->weight;
+    const int64_t room = (kRingSmem + 2048) / ring->ctas - 2048 - (int64_t)ring->weights * ring->weight;
     ring->stages = (int)std::min<int64_t>(8, room / (ring->inputs * ring->slot)) / teams * teams;
     if (ring->stages >= 2 * teams) return true;
   }
@@ -763,7 +768,7 @@ cudaError_t launch_rows(const NormGradArgs& a, const Ring& ring, cudaStream_t st
   auto* kernel = kWide      ? rows_kernel<T, W, kV, kAligned, kGrad, kTeams>
                  : a.f.even ? rows_kernel<T, W, kV, kEven, kGrad, kTeams>
                             : rows_kernel<T, W, kV, kOther, kGrad, kTeams>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring.smem());
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, dim3((unsigned)std::min(a.f.rows, ring.ctas * sm_count())),
                           dim3(ring.teams * threads_for(a.f.cols, kV) + 32), ring.smem(), st, 1, a, ring);

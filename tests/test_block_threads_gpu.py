@@ -1,0 +1,67 @@
+"""The operators around the layer called by several host threads at a time, each on
+its own stream with its own sizes: no call is refused, and the results are those of
+the same calls alone.  The C entries are called directly, so that the threads are in
+the library at the same time (Python's lock is held for a few hundred nanoseconds
+between calls)."""
+import ctypes
+import threading
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from routed_expert_ffn_forward_b200 import block, moe  # noqa: E402
+
+CALLS = 5000
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from routed_expert_ffn_forward_b200 import build
+    build.build()
+    yield
+    block.check()
+
+
+def together(calls):
+    """calls: (function of a stream that returns a status, output, the same of the call alone)."""
+    start = threading.Barrier(len(calls))
+    streams = [torch.cuda.Stream() for _ in calls]
+    statuses = [set() for _ in calls]
+    torch.cuda.synchronize()
+
+    def loop(i):
+        call, stream, seen = calls[i][0], streams[i].cuda_stream, statuses[i]
+        start.wait()
+        for _ in range(CALLS):
+            seen.add(call(stream))
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(s == {moe.MOE_OK} for s in statuses), statuses
+    assert all(torch.equal(out, want) for _, out, want in calls)
+
+
+def norm_call(rows, cols, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    h, y, post, pre = r(rows, cols), r(rows, cols), r(cols), r(cols)
+    want = block.block_norm_forward(h, y, post, None, 0.7, pre)[1]
+    a = block._norm_args(h, y, post, None, 0.7, pre, 1e-6)[0]
+    out, nxt = torch.empty_like(h), torch.empty_like(h)
+    a.out, a.next = out.data_ptr(), nxt.data_ptr()
+    keep, fn = (h, y, post, pre, out), moe.lib().moe_block_norm
+    return (lambda stream, ref=ctypes.byref(a), keep=keep: fn(ref, stream)), nxt, want
+
+
+def test_norms_of_several_widths():
+    """One kernel for all widths, with up to eight times the shared memory for the widest."""
+    together([norm_call(300, cols, cols) for cols in (4096, 1024, 2048, 520, 4096, 1024)])
