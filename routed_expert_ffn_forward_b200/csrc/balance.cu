@@ -366,9 +366,12 @@ cudaError_t forward_as(const BalanceArgs& a, cudaStream_t st) {
   const bool whole = a.tokens <= kSmallTokens && a.seqs == 1 && !a.offsets;
   const int run = whole ? std::max(a.tokens, 1) : run_length(a.tokens), runs = std::max(1, (a.tokens + run - 1) / run);
   const size_t smem = ((size_t)kWarps * padded(a.experts) + a.experts) * 4;
+  constexpr int kMost = (kWarps + 1) * 32 * kPL * 4;   // of this kernel's most experts
   auto* kernel = balance_runs_kernel<kPL, kVec>;
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (what a kernel may take is a limit of its own, not of a launch: never a call's size, which may be less than that of
+  // another thread's call)
+  if (kMost > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   if (e == cudaSuccess)
     e = launch_dependent(kernel, dim3((unsigned)runs), dim3(kWarps * 32), smem, st, 1, a, run, whole ? 1 : 0);
   if (e != cudaSuccess || whole) return e;

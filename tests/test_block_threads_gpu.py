@@ -65,3 +65,22 @@ def norm_call(rows, cols, seed):
 def test_norms_of_several_widths():
     """One kernel for all widths, with up to eight times the shared memory for the widest."""
     together([norm_call(300, cols, cols) for cols in (4096, 1024, 2048, 520, 4096, 1024)])
+
+
+def balance_call(tokens, experts, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    logits = torch.randn((tokens, experts), generator=g, device="cuda")
+    ids = torch.topk(logits, 4, 1).indices.int()
+    want, counts, slope = block.balance_loss_forward(logits, ids, 0.01, 0)
+    loss = torch.empty_like(want)
+    size = moe.moe_balance_workspace(tokens, experts, 1)
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    keep, fn = (logits, ids, counts, slope, work), moe.lib().moe_balance_loss
+    args = (logits.data_ptr(), experts, ids.data_ptr(), tokens, experts, 4, 0, None, 1, None, 0.01, loss.data_ptr(),
+            counts.data_ptr(), slope.data_ptr(), work.data_ptr(), size)
+    return (lambda stream, keep=keep: fn(*args, stream)), loss, want
+
+
+def test_balance_losses_of_several_widths():
+    """One kernel from 513 experts on, which above 722 needs more shared memory than a kernel has unasked."""
+    together([balance_call(64, experts, experts) for experts in (1024, 640, 700, 1024, 640, 900)])
