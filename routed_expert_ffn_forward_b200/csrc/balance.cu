@@ -154,7 +154,7 @@ __device__ __forceinline__ float block_sum(float v, float* s_red) {
 
 template <int kPL, bool kVec>
 __global__ void __launch_bounds__(kWarps * 32) balance_runs_kernel(const BalanceArgs a, int run, int whole) {
-  extern __shared__ float s_mem[];              // [kWarps][padded experts] sums, [experts] counts
+  extern __shared__ __align__(16) float s_mem[];   // [kWarps][padded experts] sums (stored as float4), [experts] counts
   const int width = padded(a.experts);
   int* s_c = reinterpret_cast<int*>(s_mem + kWarps * width);
   __shared__ int s_n;

@@ -149,6 +149,19 @@ def test_cluster_barriers_are_reached_by_whole_warps():
     assert uses >= 4
 
 
+def test_dynamic_shared_memory_is_aligned_to_its_widest_access():
+    """The operators access their dynamic shared memory in 16-byte words, and it says
+    so: an array of floats may be placed at any multiple of four bytes behind static
+    shared memory."""
+    import os
+    import re
+    declared = []
+    for name in ("balance.cu", "block_norm.cu", "mx_product.cu"):
+        text = open(os.path.join(os.path.dirname(build.__file__), "csrc", name)).read()
+        declared += re.findall(r"extern __shared__[^;]*;", text)
+    assert len(declared) == 3 and all("__align__(16)" in d for d in declared), declared
+
+
 def test_warps_that_stay_together_give_up_together():
     """The product's MMA and epilogue warps shuffle and load tensor memory as whole
     warps, so each of their bounded waits ends with one answer of the warp."""
