@@ -193,7 +193,6 @@ moe_status moe_mx_product(const uint8_t* codes, const uint8_t* scales, int n_x, 
   a.features = features;
   a.out_type = out_type;
   a.paired = paired != 0;
-  a.wide_store = ld % 2 == 0 && aligned(out, 2 * size);
   return launched(launch_mx_product(a, static_cast<cudaStream_t>(stream)), 1, "MXFP4 product");
 }
 

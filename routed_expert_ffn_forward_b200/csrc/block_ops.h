@@ -87,9 +87,10 @@ struct MxProductArgs {
   void* out;               // [n_rows, ld]
   int64_t ld;
   int index_div, n_x, n_rows, groups, kc, row_tiles, features, out_type;
-  bool paired, wide_store;
+  bool paired;
+  bool wide_store;         // stores of two features: the launcher's, from out, ld and out_type
 };
-cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t st);
+cudaError_t launch_mx_product(MxProductArgs a, cudaStream_t st);
 // bit flags of products whose kernel gave up on a bounded wait since the last
 // call (the GPU is idle)
 cudaError_t mx_product_errors(unsigned* flags);

@@ -982,7 +982,6 @@ moe_status forward_mx_impl(moe_layer* L, const void* x, void* out, int T, cudaSt
   a.features = s.H;
   a.out_type = kF32;
   a.paired = false;
-  a.wide_store = true;
   MOE_KERNEL(MOE_K_DOWN, launch_mx_product(a, st));
   MOE_KERNEL(MOE_K_COMBINE, launch_combine(wk, T, s, static_cast<__nv_bfloat16*>(out), st, true));
 #undef MOE_KERNEL

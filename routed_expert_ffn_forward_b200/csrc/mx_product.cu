@@ -637,8 +637,9 @@ int clusters_at_once(int cluster) {
 
 }  // namespace
 
-cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t st) {
+cudaError_t launch_mx_product(MxProductArgs a, cudaStream_t st) {
   const int sms = sm_count();
+  a.wide_store = a.ld % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % (2 * type_bytes(a.out_type)) == 0;
   // Many rows: pairs with tiles of up to 240 of them (4096 rows of 256 groups, 7168 x 4096: 674 us against 841 with
   // one CTA per unit and tiles of 112; one group of 4096 rows 52 against 65).  Fewer: tiles of 64, one CTA each (512
   // rows of one group: 16 us against 23 in pairs, which have a third of the units).

@@ -177,6 +177,19 @@ def test_warps_that_stay_together_give_up_together():
     assert len(waits) >= 6 and set(waits) <= set(agreed)
 
 
+def test_the_product_s_launcher_chooses_its_stores():
+    """Every caller of the product gets the stores that its output allows: none sets
+    them, or leaves them out, by itself."""
+    import os
+    import re
+    found = {}
+    for path in build.sources():
+        n = len(re.findall(r"\.wide_store\s*=", open(path).read()))
+        if n:
+            found[os.path.basename(path)] = n
+    assert found == {"mx_product.cu": 1}
+
+
 def test_forward_mx_refusals_without_a_layer():
     refused(BAD, moe.moe_forward_mx, None, P, P, 4)
     refused(BAD, moe.moe_set_mx_experts, None, P, P)
