@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from routed_expert_ffn_forward_b200 import block  # noqa: E402
+from tests import mx_ref  # noqa: E402
 from tests.test_mx_gpu import check_product, reference, weights  # noqa: E402
 
 
@@ -70,3 +71,29 @@ def test_products_behind_one_another_same_bits():
     got = [(i, run(i)) for i in order]
     assert all(torch.equal(out, want[i]) for i, out in got)
     block.check()
+
+
+@pytest.mark.parametrize("rows", [4, 100, 1100])
+def test_swiglu_of_fp32_outputs_is_exact_to_fp32(rows):
+    """Gates and ups that are exact in fp32 (eight E2M1 values, multiples of 2^-7 below 2^9), so that the output shows
+    silu's own arithmetic in steps of 2^-24: the exponential off by at most 2, the sum by 1/2, the division by 4 and the
+    product by 1/2, 7 in all (7.1 with their products).  Below -87.3 (1 + exp(-gate) above 2^126, where the division's
+    range ends) 0 for less than 1.1e-36."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    cols, feats = 256, 512
+    ones = torch.zeros((rows, cols), device="cuda")
+    ones[:, ::32] = 1.0                                      # one value of every run
+    x = block.mx_quantize(ones)
+    codes = torch.randint(0, 256, (1, 2 * feats, 8, 16), generator=g, device="cuda", dtype=torch.uint8)
+    codes[..., 1:] = 0
+    codes[..., 0] &= 15                                      # element 0 of the run
+    scales = torch.randint(127 - 6, 127 + 4, (1, 2 * feats, 8), generator=g, device="cuda", dtype=torch.uint8)
+    scales[:, :, 7] = 127 + 4                                # gates up to 96 and beyond
+    w = block.mx_rows(codes, scales, cols)
+    out = block.mx_product(x, block.mx_pack(w, True), out_dtype=torch.float32).double()
+    y = mx_ref.unpack(w.codes.cpu().numpy(), w.scales.cpu().numpy(), cols)[0][:, ::32].sum(1)
+    gate, up = torch.from_numpy(y[:feats]), torch.from_numpy(y[feats:])
+    assert float(gate.min()) < -80 and float(gate.max()) > 80 and bool((gate == gate.float()).all())
+    want = gate / (1 + torch.exp(-gate)) * up
+    err, bound = (out.cpu() - want).abs(), 7.1 * 2.0 ** -24 * want.abs() + 1.1e-36 * (gate < -87.3) * up.abs()
+    assert bool((err <= bound + 2.0 ** -149).all()), float((err / (bound + 2.0 ** -149)).max())
