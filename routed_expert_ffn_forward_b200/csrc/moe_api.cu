@@ -15,6 +15,7 @@
 // recorded on the compute stream after the kernels that read it, and a later
 // fill of that slot waits on it before overwriting.
 #include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <thread>
 #include <cstdio>
@@ -79,6 +80,7 @@ constexpr int kMaxTokens = 32768;
 
 std::mutex g_mu;            // guards the cache, the stats and the budget
 moe_stats g_stats{};
+std::atomic<uint64_t> g_op_launches{0};   // of the operators around the layer: part of moe_stats.launches, counted without g_mu
 size_t g_cache_bytes = SIZE_MAX;
 int g_cache_policy = MOE_CACHE_LRU;
 uint64_t g_hook_wait_ns = 0;  // moe_set_test_hooks
@@ -181,10 +183,7 @@ int moe::report_error(int status, const char* msg) {
   return status;
 }
 void moe::clear_error() { g_err.clear(); }
-void moe::count_launches(unsigned n) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  g_stats.launches += n;
-}
+void moe::count_launches(unsigned n) { g_op_launches.fetch_add(n, std::memory_order_relaxed); }
 
 struct moe_layer {
   uint32_t id = 0;
@@ -1437,6 +1436,7 @@ moe_status moe_get_stats(moe_stats* out) {
   if (!out) return fail(MOE_ERR_INVALID_ARG, "null out");
   std::lock_guard<std::mutex> lk(g_mu);
   *out = g_stats;
+  out->launches += g_op_launches.load(std::memory_order_relaxed);
   return MOE_OK;
 }
 
@@ -1445,6 +1445,7 @@ moe_status moe_reset_stats(void) {
   std::lock_guard<std::mutex> lk(g_mu);
   const uint64_t slots = g_stats.cache_slots, sb = g_stats.slot_bytes;
   g_stats = moe_stats{};
+  g_op_launches.store(0, std::memory_order_relaxed);
   g_stats.cache_slots = slots;
   g_stats.slot_bytes = sb;
   return MOE_OK;

@@ -5,6 +5,7 @@ the library at the same time (Python's lock is held for a few hundred nanosecond
 between calls)."""
 import ctypes
 import threading
+import time
 
 import pytest
 
@@ -84,3 +85,35 @@ def balance_call(tokens, experts, seed):
 def test_balance_losses_of_several_widths():
     """One kernel from 513 experts on, which above 722 needs more shared memory than a kernel has unasked."""
     together([balance_call(64, experts, experts) for experts in (1024, 640, 700, 1024, 640, 900)])
+
+
+def test_calls_do_not_wait_for_the_expert_cache():
+    """While another thread holds the cache (here: for as long as a GPU of 1.5 s of work takes, which a new cache size
+    waits for), the operators are launched and counted all the same."""
+    import dataclasses
+    from routed_expert_ffn_forward_b200 import synth
+    from routed_expert_ffn_forward_b200.layer import layer_from_config
+    moe.moe_set_cache_bytes(1 << 20)
+    L = layer_from_config(dataclasses.replace(synth.TINY, seed=3))   # streamed: the cache is there
+    try:
+        x = torch.randn((4, 256), device="cuda")
+        block.mx_quantize(x)
+        torch.cuda.synchronize()
+        before = moe.moe_get_stats()["launches"]
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(int(1.5e9 * 1.9))
+        holder = threading.Thread(target=moe.moe_set_cache_bytes, args=(1 << 20,))
+        holder.start()
+        time.sleep(0.2)
+        t = time.perf_counter()
+        for _ in range(10):
+            block.mx_quantize(x)
+        took = time.perf_counter() - t
+        waiting = holder.is_alive()
+        holder.join()
+        assert waiting and took < 0.5, (waiting, took)
+        assert moe.moe_get_stats()["launches"] == before + 10
+    finally:
+        L.destroy()
+        moe.moe_set_cache_bytes(moe.SIZE_MAX)
