@@ -765,13 +765,17 @@ cudaError_t launch_rows(const NormGradArgs& a, const Ring& ring, cudaStream_t st
   // values: by single accesses (777 x 1003: 6 us forward against 11 by shifted words; 3000 x 2998 backward 80 us,
   // by pairs 124).
   constexpr Access kOther = sizeof(T) == 2 ? kShifted : kStrided, kEven = sizeof(T) == 2 ? kPairs : kOther;
-  auto* kernel = kWide      ? rows_kernel<T, W, kV, kAligned, kGrad, kTeams>
-                 : a.f.even ? rows_kernel<T, W, kV, kEven, kGrad, kTeams>
-                            : rows_kernel<T, W, kV, kOther, kGrad, kTeams>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, dim3((unsigned)std::min(a.f.rows, ring.ctas * sm_count())),
-                          dim3(ring.teams * threads_for(a.f.cols, kV) + 32), ring.smem(), st, 1, a, ring);
+  if constexpr (sizeof(T) == 4 && !kWide && (kTeams == 2 || (kGrad && kV == 2))) {
+    return cudaErrorInvalidValue;   // ring_for chooses neither with single accesses
+  } else {
+    void (*kernel)(const NormGradArgs, const Ring);
+    if constexpr (kWide) kernel = rows_kernel<T, W, kV, kAligned, kGrad, kTeams>;
+    else kernel = a.f.even ? rows_kernel<T, W, kV, kEven, kGrad, kTeams> : rows_kernel<T, W, kV, kOther, kGrad, kTeams>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3((unsigned)std::min(a.f.rows, ring.ctas * sm_count())),
+                            dim3(ring.teams * threads_for(a.f.cols, kV) + 32), ring.smem(), st, 1, a, ring);
+  }
 }
 
 template <typename T, typename W, bool kWide>
