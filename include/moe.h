@@ -248,6 +248,11 @@ moe_status moe_set_few_row_tiles(int max_rows);
  * In streaming mode the call reads the routing back to the host (one stream
  * synchronisation) to resolve cache misses before the expert kernels are
  * launched.  out must not overlap x.
+ * A captured forward (resident mode) keeps the scratch that it was captured
+ * with until the layer is destroyed, also where a later forward at a larger T
+ * brings new scratch; the layer's forwards and its graphs' replays are for the
+ * caller to order.  After a capture moe_check and the layer's end wait for the
+ * whole GPU, since replays may run on any stream.
  * Source: LayerStoRm README, "TL;DR" (router, activated experts, combine) and
  * "Notes" (a deterministic expert combine). */
 moe_status moe_forward(moe_layer_t layer, const void* x, void* out, int T, void* stream);

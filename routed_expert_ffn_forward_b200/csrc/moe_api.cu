@@ -211,6 +211,12 @@ struct moe_layer {
   // scratch
   int T_cap = 0;
   void* scratch = nullptr;
+  bool captured = false;                // a forward was captured in a CUDA graph: replays are not seen here
+  struct OldScratch {
+    void* base;
+    unsigned *err, *sync;
+  };
+  std::vector<OldScratch> graph_scratch;   // earlier scratch that captured forwards still use, freed with the layer
   Work wk{};
   __nv_bfloat16* xbuf = nullptr;
   __nv_bfloat16* obuf = nullptr;
@@ -236,17 +242,33 @@ moe_status check_device(const moe_layer* L) {
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Wait for the layer's own outstanding work: its last forward (on whatever
-// stream it ran) and its copy stream.  Other work on the device is not waited for.
+// stream it ran) and its copy stream.  Other work on the device is not waited
+// for, unless a forward was captured: its replays may run on any stream.
 moe_status wait_layer(moe_layer* L) {
+  if (L->captured) CUDA_TRY(cudaDeviceSynchronize());
   if (L->done && L->done_rec) CUDA_TRY(cudaEventSynchronize(L->done));
   if (L->copy) CUDA_TRY(cudaStreamSynchronize(L->copy));
   return MOE_OK;
 }
 
+// Mark the end of a forward on `st`.  An event recorded in a capture can be
+// neither waited for nor queried, so a captured forward leaves it alone.
+moe_status record_done(moe_layer* L, cudaStream_t st) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  CUDA_TRY(cudaStreamIsCapturing(st, &capture));
+  if (capture != cudaStreamCaptureStatusNone) {
+    L->captured = true;
+    return MOE_OK;
+  }
+  CUDA_TRY(cudaEventRecord(L->done, st));
+  L->done_rec = true;
+  return MOE_OK;
+}
+
 // Grow the per-call scratch to hold T tokens (power of two, at least 64).
 // The old scratch may still be read by the layer's last forward, so that is
-// waited for before it is freed; the new one is zeroed on `st`, ahead of the
-// forward that needs it.
+// waited for before it is freed, and it stays if a captured forward uses it;
+// the new one is zeroed on `st`, ahead of the forward that needs it.
 moe_status ensure_scratch(moe_layer* L, int T, cudaStream_t st) {
   if (T <= L->T_cap) return MOE_OK;
   int cap = 64;
@@ -270,8 +292,12 @@ moe_status ensure_scratch(moe_layer* L, int T, cudaStream_t st) {
                o_x16 = take(P * s.H * 2), o_rinv = take(P * 4), o_h16 = take(P * s.I_pad * 2), o_hinv = take(P * 4),
                o_rpart = take(router_part_floats(cap, s.E, s.n_sm) * 4), o_sync = take(kSyncWords * 4);
   if (L->scratch) {
-    MOE_TRY(wait_layer(L));
-    cudaFree(L->scratch);
+    if (L->captured) {
+      L->graph_scratch.push_back({L->scratch, L->wk.err, L->wk.sync});
+    } else {
+      MOE_TRY(wait_layer(L));
+      cudaFree(L->scratch);
+    }
     L->scratch = nullptr;
     L->T_cap = 0;
   }
@@ -704,8 +730,7 @@ moe_status forward_impl(moe_layer* L, const void* x, void* out, int T, const int
       fa.w = wk.w + (size_t)t * s.k;
       MOE_KERNEL(MOE_K_FUSED, launch_decode1_fused(fa, s.n_sm, st));
     }
-    CUDA_TRY(cudaEventRecord(L->done, st));
-    L->done_rec = true;
+    MOE_TRY(record_done(L, st));
     if (!lk.owns_lock()) lk.lock();
     if (prof) g_prof_pending.push_back(pr);
     g_stats.launches += (uint64_t)n_launch;
@@ -867,8 +892,7 @@ moe_status forward_impl(moe_layer* L, const void* x, void* out, int T, const int
     MOE_KERNEL(MOE_K_COMBINE, launch_combine(wk, T, s, static_cast<__nv_bfloat16*>(out), st, true, partial, L->ep_rank, L->ep_world));
   }
 #undef MOE_KERNEL
-  CUDA_TRY(cudaEventRecord(L->done, st));
-  L->done_rec = true;
+  MOE_TRY(record_done(L, st));
   {
     if (!lk.owns_lock()) lk.lock();
     if (prof) g_prof_pending.push_back(pr);
@@ -984,8 +1008,7 @@ moe_status forward_mx_impl(moe_layer* L, const void* x, void* out, int T, cudaSt
   MOE_KERNEL(MOE_K_DOWN, launch_mx_product(a, st));
   MOE_KERNEL(MOE_K_COMBINE, launch_combine(wk, T, s, static_cast<__nv_bfloat16*>(out), st, true));
 #undef MOE_KERNEL
-  CUDA_TRY(cudaEventRecord(L->done, st));
-  L->done_rec = true;
+  MOE_TRY(record_done(L, st));
   std::lock_guard<std::mutex> lk(g_mu);
   if (prof) g_prof_pending.push_back(pr);
   g_stats.launches += (uint64_t)n_launch;
@@ -1100,6 +1123,7 @@ moe_status moe_layer_destroy(moe_layer_t L) {
   if (L->d_tmaps) cudaFree(L->d_tmaps);
   if (L->d_slot_of) cudaFree(L->d_slot_of);
   if (L->scratch) cudaFree(L->scratch);
+  for (auto& old : L->graph_scratch) cudaFree(old.base);
   if (L->h_ids) cudaFreeHost(L->h_ids);
   if (L->h_err) cudaFreeHost(L->h_err);
   if (L->done) cudaEventDestroy(L->done);
@@ -1414,16 +1438,23 @@ moe_status moe_check(moe_layer_t L) {
   MOE_TRY(check_device(L));
   MOE_TRY(wait_layer(L));
   if (!L->scratch) return MOE_OK;
-  CUDA_TRY(cudaMemcpyAsync(L->h_err, L->wk.err, sizeof(unsigned), cudaMemcpyDeviceToHost, L->copy));
-  CUDA_TRY(cudaStreamSynchronize(L->copy));
-  const unsigned flags = *L->h_err;
-  if (flags) {
+  unsigned flags = 0;
+  auto collect = [&](unsigned* err, unsigned* sync) -> moe_status {
+    CUDA_TRY(cudaMemcpyAsync(L->h_err, err, sizeof(unsigned), cudaMemcpyDeviceToHost, L->copy));
+    CUDA_TRY(cudaStreamSynchronize(L->copy));
+    if (!*L->h_err) return MOE_OK;
+    flags |= *L->h_err;
     // a kernel that gave up may have left its step counters half-way: start
     // them from zero again (not the launch counter, words 4-5, which stays a
     // multiple of the grid: every CTA of every launch adds 1 at its start)
-    CUDA_TRY(cudaMemsetAsync(L->wk.sync + 8, 0, (kSyncWords - 8) * sizeof(unsigned), L->copy));
-    CUDA_TRY(cudaMemsetAsync(L->wk.err, 0, sizeof(unsigned), L->copy));
+    CUDA_TRY(cudaMemsetAsync(sync + 8, 0, (kSyncWords - 8) * sizeof(unsigned), L->copy));
+    CUDA_TRY(cudaMemsetAsync(err, 0, sizeof(unsigned), L->copy));
     CUDA_TRY(cudaStreamSynchronize(L->copy));
+    return MOE_OK;
+  };
+  MOE_TRY(collect(L->wk.err, L->wk.sync));
+  for (auto& old : L->graph_scratch) MOE_TRY(collect(old.err, old.sync));
+  if (flags) {
     if (flags & kErrBoundsBit)
       return fail(MOE_ERR_CUDA, "an index a kernel read from memory was out of range (flags 0x%x)", flags);
     return fail(MOE_ERR_CUDA, "a kernel of this layer gave up waiting (flags 0x%x)", flags);
