@@ -248,7 +248,8 @@ moe_status moe_set_few_row_tiles(int max_rows);
  * In streaming mode the call reads the routing back to the host (one stream
  * synchronisation) to resolve cache misses before the expert kernels are
  * launched.  out must not overlap x.
- * A captured forward (resident mode) keeps the scratch that it was captured
+ * In a capture such a first forward is refused (NOT_READY), and the capture
+ * goes on.  A captured forward (resident mode) keeps the scratch that it was captured
  * with until the layer is destroyed, also where a later forward at a larger T
  * brings new scratch; the layer's forwards and its graphs' replays are for the
  * caller to order.  After a capture moe_check and the layer's end wait for the
@@ -281,8 +282,8 @@ moe_status moe_set_mx_experts(moe_layer_t layer, const void* gate_up, const void
  * (rounded to bf16) in MXFP4 as moe_mx_quantize gives it and fp32 sums.  Both
  * operands are 4-bit, so the output differs from moe_forward's (which keeps 16
  * bits of the activations) by the activations' rounding to E2M1, up to 1/6 of a
- * value.  Never waits for the GPU except as moe_forward's first call at a T;
- * can be captured in a CUDA graph after that.  Counts as a prefill call.
+ * value.  Never waits for the GPU except as moe_forward's first call at a T
+ * larger than any before; can be captured in a CUDA graph after that.  Counts as a prefill call.
  * Errors: as moe_forward; NOT_READY without moe_set_mx_experts, UNSUPPORTED
  * with expert parallelism.  moe_get_routing and moe_get_logits give its
  * routing; moe_block_check reports a product that gave up waiting. */

@@ -271,6 +271,11 @@ moe_status record_done(moe_layer* L, cudaStream_t st) {
 // the new one is zeroed on `st`, ahead of the forward that needs it.
 moe_status ensure_scratch(moe_layer* L, int T, cudaStream_t st) {
   if (T <= L->T_cap) return MOE_OK;
+  // (an allocation would end the capture, and zeros that a replay writes would be missing until then)
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  CUDA_TRY(cudaStreamIsCapturing(st, &capture));
+  if (capture != cudaStreamCaptureStatusNone)
+    return fail(MOE_ERR_NOT_READY, "the first forward of more than %d tokens allocates scratch and cannot be captured", L->T_cap);
   int cap = 64;
   while (cap < T) cap <<= 1;
   const Shape& s = L->s;

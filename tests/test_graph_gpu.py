@@ -72,3 +72,24 @@ def test_a_captured_forward_and_larger_batches(layer, T):
         graph2.replay()
     moe.moe_check(L.handle)
     assert torch.equal(out, want[0]) and torch.equal(out2, wide[0])
+
+
+def test_a_first_forward_in_a_capture_is_refused(layer):
+    """It would allocate scratch: refused before it does, and what was captured beside it is sound."""
+    L, forward, x = layer
+    small, big = x(8), x(100)
+    want = forward(small)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(moe.MoEError) as e:
+            forward(big)
+        out = forward(small)
+    assert e.value.status == moe.MOE_ERR_NOT_READY
+    graph.replay()
+    assert torch.equal(out, want)
+    wide = forward(big)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = forward(big)
+    graph.replay()
+    assert torch.equal(out, wide)
