@@ -272,9 +272,11 @@ moe_status moe_forward_routed(moe_layer_t layer, const void* x, void* out, int T
  * launch): gate_up and down are images of moe_mx_pack for all E + S experts,
  * gate_up of n_mats = E + S matrices [2 inter, hidden], gate rows first, with
  * paired = 1, down of [hidden, inter] with paired = 0; device memory, 16-byte
- * aligned, borrowed until the layer is destroyed or given others.  The layer
- * needs no moe_set_experts for it.  Errors: INVALID_ARG, UNSUPPORTED (E + S >
- * 1024). */
+ * aligned, borrowed until the layer is destroyed or given others: that call
+ * waits for the layer's last forward first.  A captured forward reads the images
+ * that it was captured with.  The layer needs no moe_set_experts for it.
+ * Errors: INVALID_ARG (another device's layer among them), UNSUPPORTED (E + S
+ * > 1024). */
 moe_status moe_set_mx_experts(moe_layer_t layer, const void* gate_up, const void* down);
 
 /* moe_forward over the experts of moe_set_mx_experts, any T: the router, top-k,

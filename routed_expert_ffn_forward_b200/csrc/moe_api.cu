@@ -1386,6 +1386,8 @@ moe_status moe_set_mx_experts(moe_layer_t L, const void* gate_up, const void* do
     return fail(MOE_ERR_INVALID_ARG, "the images must be 16-byte aligned");
   if (L->s.E + L->s.S > 1024)
     return fail(MOE_ERR_UNSUPPORTED, "%d experts: a product has at most 1024 matrices", L->s.E + L->s.S);
+  MOE_TRY(check_device(L));
+  if (L->mx_gate_up) MOE_TRY(wait_layer(L));   // the caller has the old images back
   L->mx_gate_up = static_cast<const uint8_t*>(gate_up);
   L->mx_down = static_cast<const uint8_t*>(down);
   return MOE_OK;

@@ -90,7 +90,9 @@ class MoELayer:
     # ------------------------------------------------------------ MXFP4 products
     def set_mx_experts(self, gate_up: block.MXWeights, down: block.MXWeights) -> None:
         """Packed MXFP4 weights of all E + S experts for ``forward_mx``: gate_up
-        [2 inter, hidden] paired (gate rows first), down [hidden, inter]."""
+        [2 inter, hidden] paired (gate rows first), down [hidden, inter].  Others
+        than before: waits for the layer's last forward; the old ones have to be
+        kept for forwards captured with them."""
         n = self.E + self.S
         want = ((n, 2 * self.I, self.H, True), (n, self.H, self.I, False))
         for name, w, shape in zip(("gate_up", "down"), (gate_up, down), want):

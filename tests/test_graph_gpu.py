@@ -93,3 +93,24 @@ def test_a_first_forward_in_a_capture_is_refused(layer):
         out = forward(big)
     graph.replay()
     assert torch.equal(out, wide)
+
+
+def test_other_mx_experts_wait_for_the_last_forward(layer):
+    """The old images are the caller's again when the call returns."""
+    L, forward, x = layer
+    if forward.__name__ != "forward_mx":
+        pytest.skip("MXFP4 experts")
+    v = x(8)
+    want, old = forward(v), L.mx
+    new = tuple(w._replace(image=w.image.clone()) for w in old)
+    torch.cuda.synchronize()
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(0.3e9 * 1.9))
+        out = forward(v)
+        done.record()
+    L.set_mx_experts(*new)
+    assert done.query()
+    for w in old:
+        w.image.zero_()
+    assert torch.equal(out, want) and torch.equal(forward(v), want)
