@@ -283,8 +283,9 @@ moe_status moe_set_mx_experts(moe_layer_t layer, const void* gate_up, const void
  * permutation and combine of the prefill path, with x and the SwiGLU output
  * (rounded to bf16) in MXFP4 as moe_mx_quantize gives it and fp32 sums.  Both
  * operands are 4-bit, so the output differs from moe_forward's (which keeps 16
- * bits of the activations) by the activations' rounding to E2M1, up to 1/6 of a
- * value.  Never waits for the GPU except as moe_forward's first call at a T
+ * bits of the activations) by the activations' rounding to E2M1: with s the
+ * scale of a run of 32, up to 1/4 of a value above 6 s, 1/5 of one from s to 6 s,
+ * and s / 4 of smaller ones.  Never waits for the GPU except as moe_forward's first call at a T
  * larger than any before; can be captured in a CUDA graph after that.  Counts as a prefill call.
  * Errors: as moe_forward; NOT_READY without moe_set_mx_experts, UNSUPPORTED
  * with expert parallelism.  moe_get_routing and moe_get_logits give its
@@ -523,7 +524,11 @@ moe_status moe_block_norm_grad(const moe_norm_args* args, const moe_norm_grads* 
  *   f[s, i] = experts * counts[s, i] / (top_k n_s)
  *   loss = coef * mean over s with n_s > 0 of sum_i f[s, i] * mean_t p[t, i]
  *   slope[s, i] = coef * f[s, i] / (n_s * number of those s)   fp32 [seqs, experts]
- * The loss is 0 without a token that counts.  moe_balance_loss_grad: the gradient
+ * The loss is 0 without a token that counts.  Probabilities take the fast
+ * exponential: within 80 steps of 2^-24, and 4 more for each unit that their
+ * logit lies below the row's largest (softmax) or that it and the largest lie
+ * below zero (sigmoid); an exponential or sigmoid below 1.2e-38 counts as 0.
+ * Sums over tokens are fp32, in a fixed order.  moe_balance_loss_grad: the gradient
  * of the logits, fp32 [tokens, experts], times *d_loss (device; NULL: 1),
  * with the counts as constants; rows that do not count are zeros.
  * tokens 0..2^24, experts 1..1024, top_k 1..32, seqs 1..65535; workspace

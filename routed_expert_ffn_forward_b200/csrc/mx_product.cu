@@ -27,8 +27,8 @@
 // to 8 CTAs shares a unit, each takes a part of K, and the partial sums are
 // added from the CTAs' shared memory in rank order.
 //
-// Measured: one token of 8 experts, 7168 x 4096: 20.7 us, 6.0 TB/s of weights;
-// 64 tokens of 54 experts, 2048 x 7168, 68 us, 6.2 TB/s; a step of 240 rows
+// Measured: one token of 8 experts, 7168 x 4096: 19.0 us, 6.6 TB/s of weights;
+// 64 tokens of 54 experts, 2048 x 7168, 64 us, 6.6 TB/s; a step of 240 rows
 // runs at the MMAs' own rate (960 cycles), and what a unit of many rows loses
 // is its epilogue: its accumulators fill tensor memory.
 #include <atomic>
@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
   if (tid == 0) {
     // a stage is full with its weights and the copies of every row thread; that
     // the second CTA's is, the first learns on a barrier of its own (on this one
-    // its arrivals took longer: 767 against 655 us for 4096 tokens)
+    // its arrivals took longer: 1.17 times the product's time for 4096 tokens of
+    // 256 experts, both on one box, before the epilogue was what it is now)
     for (int i = 0; i < kNS; ++i) {
       ptx::mbar_init(&full[i], 1 + kRowWarps * 32);
       ptx::mbar_init(&empty[i], 1);
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_product_kernel(const MxProduct
             ptx::bulk_load(sm + (size_t)s * C::kStage, src + (int64_t)k * kMxBlockBytes, kMxBlockBytes, &full[s]);
           log.note(s, ph);
           // a CTA with one unit: the block behind the ring on its way to L2 (one token of 8 experts, 7168 x 4096:
-          // 20.7 us against 24.8).  With more units it costs more L2 than it gains.
+          // 18.8 us against 22.2).  With more units it costs more L2 than it gains.
           if (alone && k + kNS + 1 < k1) ptx::bulk_prefetch(src + (int64_t)(k + kNS + 1) * kMxBlockBytes, kMxBlockBytes);
         }
       }
@@ -645,14 +646,15 @@ int clusters_at_once(int cluster) {
 cudaError_t launch_mx_product(MxProductArgs a, cudaStream_t st) {
   const int sms = sm_count();
   a.wide_store = a.ld % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % (2 * type_bytes(a.out_type)) == 0;
-  // Many rows: pairs with tiles of up to 240 of them (4096 rows of 256 groups, 7168 x 4096: 674 us against 841 with
-  // one CTA per unit and tiles of 112; one group of 4096 rows 52 against 65).  Fewer: tiles of 64, one CTA each (512
-  // rows of one group: 16 us against 23 in pairs, which have a third of the units).
+  // Many rows: pairs with tiles of up to 240 of them; fewer: tiles of 64, one CTA each, which are more units.  Pairs
+  // against single CTAs, us: 4096 tokens of 8 of 256 groups, 7168 x 4096, 777 and 929; one group, 2048 x 7168: 4096 rows
+  // 44..53 and 55..62, 2048 rows 25 and 33, 1100 rows 16 and 18, 512 rows 13 and 11.  The rule goes by the rows alone: few
+  // features leave pairs without units (one group of 4096 rows, 2048 x 1024: 13.5 and 11.2, 2048 x 512: 13.1 and 7.4).
   if (a.n_rows > 1024 && a.row_tiles > 1) return launch<240, 4, 2, kPair>(a, 2, sms / 2, st);
   // at most this many units (up to 64 rows are one tile of any group)
   const int64_t units = (int64_t)std::min(a.n_rows <= 64 ? a.groups : a.groups + a.n_rows / 64, a.n_rows) * a.row_tiles;
   int cluster = 1;
-  // in one wave (16 clusters of 8 are two: 7168 x 4096, one row, 12.6 us, as without a cluster; 7.6 us in 16 of 4)
+  // in one wave (16 clusters of 8 are two: 7168 x 4096, one row, 12.6 us; 7.2 us in 16 of 4, 11.6 without clusters)
   if (a.n_rows <= 64 && units * 2 <= sms)
     for (int c = 8; c > 1 && cluster == 1; c /= 2)
       if (a.kc >= c * 2 && units <= clusters_at_once(c)) cluster = c;

@@ -119,6 +119,23 @@ def test_balance_many_tokens(sigmoid, tokens, experts, top_k):
     check_balance(logits, ids, sigmoid, offsets, mask)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("experts,scale,shift", [(8, 1.0, 0.0), (8, 15.0, 0.0), (1000, 3.0, 0.0), (256, 6.0, -40.0), (64, 4.0, 30.0)])
+def test_balance_probabilities_one_by_one(sigmoid, experts, scale, shift):
+    """One token that picked one expert: the loss is coef * experts times that expert's probability.  The documented
+    bound, and 6 steps for the factors."""
+    g = torch.Generator(device="cuda").manual_seed(experts)
+    logits = torch.randn((60, experts), generator=g, device="cuda") * scale + shift
+    pick = torch.randint(0, experts, (60, 1), generator=g, device="cuda", dtype=torch.int32)
+    got = torch.stack([block.balance_loss_forward(l[None], i[None], 1.0, 1 if sigmoid else 0)[0] for l, i in zip(logits, pick)])
+    l = logits.double()
+    want = ref.probabilities(l, sigmoid).gather(1, pick.long())[:, 0] * experts
+    top, mine = l.max(1).values, l.gather(1, pick.long())[:, 0]
+    units = (-mine).clamp(min=0) + (-top).clamp(min=0) if sigmoid else top - mine
+    bound = (86 + 4 * units) * U * want + experts * 1.2e-38 / (torch.sigmoid(l).sum(1) if sigmoid else 1.0)
+    assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).max())
+
+
 # ---------------------------------------------------------------- first calls
 FIRST_CALLS_CAPTURED = """
 import torch
